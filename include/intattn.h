@@ -384,6 +384,84 @@ int intattn_decode_static_scratch(const int8_t *q, const int8_t *k_cache, const 
                                   const intattn_scales_t *scales, int B, int H, int Lk, int Lmax, int d,
                                   float clip_c, int8_t *out, intattn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rows between the projections and the KV caches.
+ *
+ * A strided tensor of rows: element (b, h, t, c) of [B, heads, L, d] at
+ * ptr + b stride_b + h stride_h + t stride_l + c, strides in elements.  ptr
+ * is 16-byte aligned and the strides are multiples of 8 (a [B, L, heads, d]
+ * view of a packed projection qualifies).  An output may not repeat rows. */
+typedef struct intattn_rows {
+    const void *ptr;
+    int64_t stride_b, stride_h, stride_l;
+} intattn_rows_t;
+
+/* The norm of each query and key head and the position rotation.
+ *   norm:     y = x / sqrt(mean_c x_c^2 + eps) * w_c over the d channels of a
+ *             row, w = w_q for queries and w_k for keys (DEVICE fp32 [d], 16-byte
+ *             aligned; NULL: those rows are not normed, eps is then not read);
+ *   rotation: channels (f, f + rot/2), or (2f, 2f + 1) with interleaved, of the
+ *             first rot channels turn by the angle of their position p:
+ *             (a, b) -> (a c - b s, a s + b c), (c, s) = table[p][f].
+ *             table: DEVICE fp32 [n_positions, rot/2, 2], 16-byte aligned
+ *             (NULL: no rotation); rot a multiple of 16, <= d; positions:
+ *             DEVICE int32 [B, L].  A row whose position is negative is
+ *             padding: it is neither read nor written.  A position >=
+ *             n_positions leaves its rows unwritten and is reported by
+ *             intattn_device_error (INTATTN_ERR_PARAM_RANGE).
+ * All of it in fp32. */
+typedef struct intattn_rope_norm {
+    const float *w_q, *w_k;
+    float eps;               /* finite, > 0 */
+    const float *table;
+    int32_t n_positions;
+    int32_t rot;
+    int32_t interleaved;
+    const int32_t *positions;
+} intattn_rope_norm_t;
+
+/* Norm and rotation of q [B, H, L, d] and k [B, Hkv, L, d] (dtype
+ * INTATTN_DTYPE_FP16 or INTATTN_DTYPE_BF16) into q_out and k_out of the same type, one
+ * rounding per element: what intattn_quantize and intattn_forward_fp take.
+ * Hkv == 0 with k == k_out == NULL: queries only.  In place (an output equal
+ * to its input, strides too) is allowed, any other overlap is not.  One
+ * launch, asynchronous on `stream`. */
+int intattn_qk_norm_rope(const intattn_rows_t *q, const intattn_rows_t *k, const intattn_rope_norm_t *rn, int dtype,
+                         int B, int H, int Hkv, int L, int d, const intattn_rows_t *q_out,
+                         const intattn_rows_t *k_out, intattn_stream_t stream);
+
+/* Quantises new K and V rows with the caches' fixed scales as they are
+ * written (the scales intattn_decode and intattn_decode_int4 read the cache
+ * with), and optionally the step's queries.
+ *   k, v [B, Hkv, L, d], q [B, H, L, d] or NULL: dtype fp16 or bf16.
+ *   code = clamp(rint(RN32(x RN32(1 / s))) + z, lo, hi), ties to even;
+ *   symmetric (no zero-points): z = 0, [lo, hi] = [-127, 127] or, bits = 4,
+ *   [-7, 7]; with zero-points: [0, 255] or [0, 15].  An infinity saturates, a NaN
+ *   becomes the code of 0.
+ *   scales: s_k, s_v (and z_k, z_v) hold Hkv entries per head, s_q H; s_o and clip_c are not
+ *   read.  rn != NULL: norm and rotation of q and k (not v) come
+ *   first, in fp32 without a rounding between.
+ *   Row t of sequence b, t < lengths[b] (DEVICE int32 [B]; NULL: L), goes to
+ *   cache row start[b] + t (DEVICE int32 [B]) of k_cache, v_cache [B, Hkv, Lmax, d]
+ *   (bits = 4: d/2 bytes a row, packed as intattn_decode_int4 reads them), and to row t of
+ *   q_out [B, H, L, d] int8.  Every other row is left as it was.  A cache row outside
+ *   [0, Lmax) is not written (nor its q_out row) and is reported by
+ *   intattn_device_error (INTATTN_ERR_PARAM_RANGE).
+ * One launch, asynchronous on `stream`. */
+int intattn_cache_write(const intattn_rows_t *k, const intattn_rows_t *v, const intattn_rows_t *q, int dtype,
+                        const intattn_scales_t *scales, int bits, const intattn_rope_norm_t *rn, int B, int H,
+                        int Hkv, int L, int Lmax, int d, const int32_t *start, const int32_t *lengths, void *k_cache,
+                        void *v_cache, int8_t *q_out, intattn_stream_t stream);
+
+/* The values of cache rows: row t < lengths[b] (NULL: L) of sequence b of
+ * k_out, v_out [B, Hkv, L, d] (contiguous, dtype fp16 or bf16) receives
+ * RN(RN32(s (code - z))) of cache row start[b] + t.  scales, bits, start, lengths and rows out
+ * of range: as intattn_cache_write.  v_cache == v_out == NULL: K only.  One
+ * launch, asynchronous on `stream`. */
+int intattn_cache_read(const void *k_cache, const void *v_cache, const intattn_scales_t *scales, int bits, int B,
+                       int Hkv, int L, int Lmax, int d, const int32_t *start, const int32_t *lengths, int dtype,
+                       void *k_out, void *v_out, intattn_stream_t stream);
+
 /* Diagnostic for the failure detection: launches one CTA whose wait on a
  * barrier can never complete.  The wait gives up after the kernels' time
  * limit (2 s) and sets the device error word, so a following
@@ -394,7 +472,8 @@ int intattn_selftest_timeout(intattn_stream_t stream);
 /* Synchronises `stream`, then returns and clears the device error word that a
  * kernel sets when one of its bounded waits runs out (INTATTN_ERR_TIMEOUT) or
  * when parameters derived on the device are out of range
- * (INTATTN_ERR_PARAM_RANGE, see intattn_forward_fp), or INTATTN_OK.
+ * (INTATTN_ERR_PARAM_RANGE, see intattn_forward_fp) or a position, cache row
+ * or length read on the device is, or INTATTN_OK.
  * INTATTN_ERR_CUDA if the synchronisation itself fails. */
 int intattn_device_error(intattn_stream_t stream);
 

@@ -28,7 +28,7 @@ EXPORTED = ("intattn_derive_params", "intattn_forward", "intattn_forward_variant
             "intattn_calibrate_workspace_size", "intattn_calibrate_clip",
             "intattn_forward_host", "intattn_decode_workspace_size",
             "intattn_decode", "intattn_decode_int4", "intattn_decode_static_scratch", "intattn_quantize",
-            "intattn_quantize_zp",
+            "intattn_quantize_zp", "intattn_qk_norm_rope", "intattn_cache_write", "intattn_cache_read",
             "intattn_gelu_derive_params", "intattn_gelu", "intattn_selftest_timeout", "intattn_device_error",
             "intattn_strerror")
 DTYPE_FP16, DTYPE_BF16 = 0, 1
@@ -61,6 +61,17 @@ class _Scales(ctypes.Structure):
 class _HeadParams(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int32), ("s", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("Mo", ctypes.c_int32), ("so", ctypes.c_int32)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p),
+                ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("stride_l", ctypes.c_int64)]
+
+
+class _RopeNorm(ctypes.Structure):
+    _fields_ = [("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("table", ctypes.c_void_p), ("n_positions", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p)]
 
 
 FloatArg = Union[float, Sequence[float], np.ndarray]
@@ -148,6 +159,11 @@ def lib() -> ctypes.CDLL:
                                                     i32, i32, f32, vp, vp]
         L.intattn_quantize.argtypes = [vp, i32, i32, i32, i32, i32, i32, vp, vp, vp]
         L.intattn_quantize_zp.argtypes = [vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        rows, rn, scp = ctypes.POINTER(_Rows), ctypes.POINTER(_RopeNorm), ctypes.POINTER(_Scales)
+        L.intattn_qk_norm_rope.argtypes = [rows, rows, rn, i32, i32, i32, i32, i32, i32, rows, rows, vp]
+        L.intattn_cache_write.argtypes = [rows, rows, rows, i32, scp, i32, rn, i32, i32, i32, i32, i32, i32, vp, vp,
+                                          vp, vp, vp, vp]
+        L.intattn_cache_read.argtypes = [vp, vp, scp, i32, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp]
         L.intattn_gelu_derive_params.argtypes = [f32, f32, f32, ctypes.POINTER(_GeluParams)]
         L.intattn_gelu.argtypes = [vp, vp, ctypes.c_longlong, f32, f32, f32, vp]
         L.intattn_selftest_timeout.argtypes = [vp]
@@ -475,6 +491,266 @@ def quantize_zp(x, per_head: bool, out=None, scales=None, zero_points=None, stre
                                      scales.data_ptr(), zero_points.data_ptr(), _stream_handle(stream, x.device)),
            "intattn_quantize_zp")
     return out, scales, zero_points
+
+
+# ------------------------------------------------ rows, caches and their decode
+
+class _On:
+    """Makes `device` and `stream` (None: the device's current stream) current
+    for a call, so that what the call allocates belongs to the stream it runs
+    on; gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guards = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        self.device, self.stream = device, stream
+
+    def __enter__(self) -> int:
+        import torch
+        for g in self.guards:
+            g.__enter__()
+        s = self.stream
+        if s is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if not hasattr(s, "cuda_stream"):
+            s = torch.cuda.ExternalStream(int(s), device=self.device)
+        g = torch.cuda.stream(s)
+        g.__enter__()
+        self.guards.append(g)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _check_entries(scales: Scales, n_q: int, n_kv: int, names):
+    """The named scale arrays hold an entry per head (n_q query heads, n_kv
+    K / V heads), or one each."""
+    for name in names:
+        x = getattr(scales, name)
+        if x is None:
+            continue
+        want = (n_q if name in ("s_q", "s_o", "clip") else n_kv) if scales.per_head else 1
+        if np.size(x) < want:
+            raise ValueError(f"scales.{name} holds {np.size(x)} entries; {want} are needed")
+
+
+def _rows(t, name: str, device, dtype, heads=None) -> _Rows:
+    """A [B, heads, L, d] fp16 / bf16 CUDA tensor whose channels are contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{name} must be a CUDA float16 or bfloat16 tensor")
+    if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
+        raise ValueError(f"{name} must be [B, heads, L, d] with contiguous channels")
+    if t.device != device or t.dtype != dtype:
+        raise ValueError(f"{name} must be on {device} in {dtype}")
+    sb, sh, sl, _ = t.stride()
+    B, h, L, _ = t.shape
+    # the stride of an extent of one is never used
+    return _Rows(t.data_ptr(), sb if B > 1 else 0, sh if h > 1 else 0, sl if L > 1 else 0)
+
+
+def _index_tensor(t, name: str, shape, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
+        raise TypeError(f"{name} must be an int32 tensor on {device}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}")
+    return t.data_ptr()
+
+
+@dataclasses.dataclass
+class RopeNorm:
+    """Norm and rotation of query and key rows (intattn_rope_norm_t).
+    table: float32 CUDA [n_positions, rot/2, 2] of (cos, sin) (see rope_table;
+    None: no rotation); positions: int32 CUDA [B, L], negative = padding;
+    w_q, w_k: float32 CUDA [d] norm weights (None: not normed)."""
+    table: Optional[object] = None
+    positions: Optional[object] = None
+    w_q: Optional[object] = None
+    w_k: Optional[object] = None
+    eps: float = 1e-6
+    interleaved: bool = False
+
+    def _c(self, B: int, L: int, d: int, device) -> _RopeNorm:
+        import torch
+        c = _RopeNorm(eps=float(self.eps), interleaved=int(bool(self.interleaved)))
+        for name in ("w_q", "w_k"):
+            w = getattr(self, name)
+            if w is not None:
+                if not isinstance(w, torch.Tensor) or w.dtype != torch.float32 or w.device != device:
+                    raise TypeError(f"{name} must be a float32 tensor on {device}")
+                if w.shape != (d,) or not w.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous [{d}]")
+                setattr(c, name, w.data_ptr())
+        if self.table is not None:
+            t = self.table
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device:
+                raise TypeError(f"table must be a float32 tensor on {device}")
+            if t.dim() != 3 or t.shape[2] != 2 or not t.is_contiguous():
+                raise ValueError("table must be contiguous [n_positions, rot / 2, 2]")
+            c.table, c.n_positions, c.rot = t.data_ptr(), t.shape[0], 2 * t.shape[1]
+            c.positions = _index_tensor(self.positions, "positions", (B, L), device)
+        return c
+
+
+def rope_table(n_positions: int, rot: int, base: float = 10000.0, device="cuda"):
+    """(cos, sin) of p base^(-2 f / rot) for p < n_positions, f < rot / 2, as
+    RopeNorm takes them: float32 [n_positions, rot/2, 2], the angles in double."""
+    import torch
+    if n_positions < 1 or rot < 2 or rot % 2:
+        raise ValueError("rope_table needs n_positions >= 1 and an even rot >= 2")
+    f = float(base) ** (-torch.arange(0, rot, 2, device=device, dtype=torch.float64) / rot)
+    a = torch.arange(n_positions, device=device, dtype=torch.float64)[:, None] * f
+    return torch.stack([a.cos(), a.sin()], dim=-1).float().contiguous()
+
+
+def qk_norm_rope(q, k, norm: RopeNorm, q_out=None, k_out=None, stream=None):
+    """(q_out, k_out): norm and position rotation of fp16 / bf16 q [B, H, L, d]
+    and k [B, Hkv, L, d] (strided views with contiguous channels; k None:
+    queries only) in one pass.  In place: q_out=q, k_out=k."""
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise TypeError("q must be a CUDA tensor [B, H, L, d]")
+    dev, dt = q.device, q.dtype
+    qr = _rows(q, "q", dev, dt)
+    B, H, L, d = q.shape
+    kr = kor = None
+    Hkv = 0
+    if k is not None:
+        kr = _rows(k, "k", dev, dt)
+        Hkv = k.shape[1]
+        if k.shape != (B, Hkv, L, d):
+            raise ValueError("k must be [B, Hkv, L, d] matching q")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    c = norm._c(B, L, d, dev)
+    with _On(dev, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((B, H, L, d), dtype=dt, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty((B, Hkv, L, d), dtype=dt, device=dev)
+        qor = _rows(q_out, "q_out", dev, dt)
+        if k is not None:
+            kor = _rows(k_out, "k_out", dev, dt)
+        if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+            raise ValueError("outputs must match q and k")
+        _check(lib().intattn_qk_norm_rope(qr, kr, c, DTYPE_BF16 if dt == torch.bfloat16 else DTYPE_FP16, B, H, Hkv, L,
+                                          d, qor, kor, st), "intattn_qk_norm_rope")
+    return q_out, k_out
+
+
+def _check_cache(t, name: str, zero_point, bits: int, B: int, Hkv: int, d: int, device):
+    import torch
+    if bits not in (8, 4):
+        raise ValueError("bits must be 8 or 4")
+    want = torch.uint8 if bits == 4 or zero_point is not None else torch.int8
+    if not isinstance(t, torch.Tensor) or t.dtype != want or t.device != device:
+        raise TypeError(f"{name} must be a {want} tensor on {device}")
+    if t.dim() != 4 or t.shape[:2] != (B, Hkv) or t.shape[3] != d * bits // 8 or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{B}, {Hkv}, Lmax, {d * bits // 8}]")
+
+
+def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bits: int = 8, q=None, q_out=None,
+                norm: Optional[RopeNorm] = None, stream=None):
+    """Quantises fp16 / bf16 rows k, v [B, Hkv, L, d] (strided views) with the
+    caches' fixed scales into cache rows start[b] + t, t < lengths[b] (int32
+    CUDA [B]; None: L).  k_cache, v_cache: [B, Hkv, Lmax, d] int8 (uint8 with
+    zero-points), or, bits = 4, uint8 [B, Hkv, Lmax, d/2].  q [B, H, L, d]:
+    also the step's queries, with scales.s_q, into int8 q_out (returned).
+    norm: norm and rotation of q and k first, in the same pass."""
+    import torch
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise TypeError("k must be a CUDA tensor [B, Hkv, L, d]")
+    dev, dt = k.device, k.dtype
+    kr, vr = _rows(k, "k", dev, dt), _rows(v, "v", dev, dt)
+    B, Hkv, L, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("v must match k")
+    _check_cache(k_cache, "k_cache", scales.z_k, bits, B, Hkv, d, dev)
+    _check_cache(v_cache, "v_cache", scales.z_v, bits, B, Hkv, d, dev)
+    Lmax = k_cache.shape[2]
+    if v_cache.shape[2] != Lmax:
+        raise ValueError("the caches must have one capacity")
+    H, qr = 0, None
+    if q is not None:
+        qr = _rows(q, "q", dev, dt)
+        H = q.shape[1]
+        if q.shape != (B, H, L, d):
+            raise ValueError("q must be [B, H, L, d] matching k")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check_entries(scales, H, Hkv, ("s_k", "s_v", "z_k", "z_v") + (("s_q",) if q is not None else ()))
+    sp = _index_tensor(start, "start", (B,), dev)
+    lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
+    c = None if norm is None else norm._c(B, L, d, dev)
+    sc, keep = scales._c()
+    with _On(dev, stream) as st:
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty((B, H, L, d), dtype=torch.int8, device=dev)
+            _check_tensor(q_out, "q_out")
+            if q_out.shape != q.shape or q_out.device != dev:
+                raise ValueError("q_out must match q")
+        rc = lib().intattn_cache_write(kr, vr, qr, DTYPE_BF16 if dt == torch.bfloat16 else DTYPE_FP16, sc, int(bits), c,
+                                       B, H, Hkv, L, Lmax, d, sp, lp, k_cache.data_ptr(), v_cache.data_ptr(),
+                                       None if q is None else q_out.data_ptr(), st)
+    del keep
+    _check(rc, "intattn_cache_write")
+    return q_out
+
+
+def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bits: int = 8, dtype=None, k_out=None,
+               v_out=None, stream=None):
+    """(k_out, v_out): the values of cache rows start[b] + t, t < lengths[b]
+    (None: L), as fp16 / bf16 [B, Hkv, L, d] (dtype; default bf16).  Rows past
+    lengths[b] are left as they were.  v_cache None: K only."""
+    import torch
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or not k_cache.is_cuda:
+        raise TypeError("k_cache must be a CUDA tensor [B, Hkv, Lmax, d]")
+    if bits not in (8, 4):
+        raise ValueError("bits must be 8 or 4")
+    dev = k_cache.device
+    B, Hkv, Lmax, d = k_cache.shape
+    d = d * 8 // bits
+    L = int(L)
+    if L < 0:
+        raise ValueError("L must not be negative")
+    _check_cache(k_cache, "k_cache", scales.z_k, bits, B, Hkv, d, dev)
+    if v_cache is not None:
+        _check_cache(v_cache, "v_cache", scales.z_v, bits, B, Hkv, d, dev)
+        if v_cache.shape != k_cache.shape:
+            raise ValueError("the caches must match")
+    elif v_out is not None:
+        raise ValueError("v_out without v_cache")
+    dt = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
+    if dt not in (torch.float16, torch.bfloat16):
+        raise TypeError("dtype must be float16 or bfloat16")
+    _check_entries(scales, 0, Hkv, ("s_k", "z_k") + (("s_v", "z_v") if v_cache is not None else ()))
+    sp = _index_tensor(start, "start", (B,), dev)
+    lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
+    sc, keep = scales._c()
+    with _On(dev, stream) as st:
+        if k_out is None:
+            k_out = torch.empty((B, Hkv, L, d), dtype=dt, device=dev)
+        if v_out is None and v_cache is not None:
+            v_out = torch.empty((B, Hkv, L, d), dtype=dt, device=dev)
+        for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is None:
+                continue
+            if not isinstance(t, torch.Tensor) or t.dtype != dt or t.device != dev:
+                raise TypeError(f"{n} must be a {dt} tensor on {dev}")
+            if t.shape != (B, Hkv, L, d) or not t.is_contiguous():
+                raise ValueError(f"{n} must be contiguous {[B, Hkv, L, d]}")
+        rc = lib().intattn_cache_read(k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), sc, int(bits),
+                                      B, Hkv, L, Lmax, d, sp, lp, DTYPE_BF16 if dt == torch.bfloat16 else DTYPE_FP16,
+                                      k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), st)
+    del keep
+    _check(rc, "intattn_cache_read")
+    return k_out, v_out
 
 
 def gelu_params(s_x: float, s_y: float, c: float):

@@ -25,6 +25,7 @@
 #include "quantize_kernel.cuh"
 #include "prefill_kernel.cuh"
 #include "prefill_short_kernel.cuh"
+#include "rows_kernel.cuh"
 
 using intattn::DecodeArgs;
 using intattn::HeadParamsDev;
@@ -961,6 +962,8 @@ int quantize_impl(const void* x, int dtype, int B, int H, int L, int d, int per_
 }
 
 }  // namespace
+
+#include "rows_api.cuh"
 
 extern "C" {
 
