@@ -208,8 +208,9 @@ int intattn_decode_int4(const int8_t *q, const uint8_t *k_cache, const uint8_t *
                         float clip_c, int8_t *out, void *workspace, size_t workspace_bytes,
                         intattn_stream_t stream);
 
-/* Element types accepted by intattn_quantize. */
-enum { INTATTN_DTYPE_FP16 = 0, INTATTN_DTYPE_BF16 = 1 };
+/* Element types accepted by intattn_quantize (INTATTN_DTYPE_INT8: an output
+ * type of intattn_decode_shared only). */
+enum { INTATTN_DTYPE_FP16 = 0, INTATTN_DTYPE_BF16 = 1, INTATTN_DTYPE_INT8 = 2 };
 
 /* Quantisation prologue (the step upstream of the integer pipeline: the
  * forum page "IntAttention：面向边缘设备的纯整数注意力推理加速方案", section
@@ -461,6 +462,37 @@ int intattn_cache_write(const intattn_rows_t *k, const intattn_rows_t *v, const 
 int intattn_cache_read(const void *k_cache, const void *v_cache, const intattn_scales_t *scales, int bits, int B,
                        int Hkv, int L, int Lmax, int d, const int32_t *start, const int32_t *lengths, int dtype,
                        void *k_out, void *v_out, intattn_stream_t stream);
+
+/* Bytes of device workspace intattn_decode_shared needs (0 for invalid sizes). */
+size_t intattn_decode_shared_workspace_size(int B, int H, int Hkv, int Lmax, int d);
+
+/* Decode for a batch whose sequences share a prefix (a system prompt, a
+ * document): one query per (b, h) against the keys of the prefix, held and read once
+ * for all sequences, followed by the keys of the sequence's own cache.  The
+ * definition above with Lq = 1 and no mask over the joined keys
+ *   prefix[hk, 0 .. Lp), cache[b, hk, 0 .. lengths[b]),   hk = h / (H / Hkv):
+ * the bytes of intattn_decode on the joined cache.  Grouped heads: H is a
+ * multiple of Hkv, and scales s_q, s_o and clip_c hold H entries per head,
+ * s_k, s_v, z_k and z_v Hkv.
+ *   q [B, H, 1, d] int8; k_prefix, v_prefix [Hkv, Lp_max, d], the first Lp rows valid;
+ *   k_cache, v_cache [B, Hkv, Lmax, d]; int8, or u8 with zero-points (prefix and
+ *   caches share scales and zero-points).
+ *   lengths: DEVICE int32 [B], 0 <= lengths[b] <= Lmax, or NULL: Lmax.  A length out of
+ *   range leaves the sequence's output unwritten and is reported by
+ *   intattn_device_error (INTATTN_ERR_PARAM_RANGE).  A sequence without any
+ *   key gives 0.
+ *   1 <= Lp + Lmax <= 65535; with Lp (Lmax) 0 the prefix (cache) may be NULL.
+ *   out [B, H, 1, d]: out_dtype INTATTN_DTYPE_INT8: the codes of the definition; INTATTN_DTYPE_FP16
+ *   or INTATTN_DTYPE_BF16: the values RN(RN32(s_o code)) they stand for.
+ *   workspace: device, 256-byte aligned, at least
+ *   intattn_decode_shared_workspace_size bytes; contents need no
+ *   initialisation; calls (and graphs) that share it must be ordered on one
+ *   stream.  Return codes: as intattn_decode. */
+int intattn_decode_shared(const int8_t *q, const int8_t *k_prefix, const int8_t *v_prefix, int Lp, int Lp_max,
+                          const int8_t *k_cache, const int8_t *v_cache, const int32_t *lengths,
+                          const intattn_scales_t *scales, int B, int H, int Hkv, int Lmax, int d, float clip_c,
+                          int out_dtype, void *out, void *workspace, size_t workspace_bytes,
+                          intattn_stream_t stream);
 
 /* Diagnostic for the failure detection: launches one CTA whose wait on a
  * barrier can never complete.  The wait gives up after the kernels' time

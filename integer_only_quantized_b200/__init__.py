@@ -29,9 +29,10 @@ EXPORTED = ("intattn_derive_params", "intattn_forward", "intattn_forward_variant
             "intattn_forward_host", "intattn_decode_workspace_size",
             "intattn_decode", "intattn_decode_int4", "intattn_decode_static_scratch", "intattn_quantize",
             "intattn_quantize_zp", "intattn_qk_norm_rope", "intattn_cache_write", "intattn_cache_read",
+            "intattn_decode_shared_workspace_size", "intattn_decode_shared",
             "intattn_gelu_derive_params", "intattn_gelu", "intattn_selftest_timeout", "intattn_device_error",
             "intattn_strerror")
-DTYPE_FP16, DTYPE_BF16 = 0, 1
+DTYPE_FP16, DTYPE_BF16, DTYPE_INT8 = 0, 1, 2
 VARIANT_AUTO, VARIANT_THREE_PASS, VARIANT_SHORT_ROWS = 0, 1, 2
 SHORT_ROWS_MAX_KEYS = 256
 
@@ -164,6 +165,10 @@ def lib() -> ctypes.CDLL:
         L.intattn_cache_write.argtypes = [rows, rows, rows, i32, scp, i32, rn, i32, i32, i32, i32, i32, i32, vp, vp,
                                           vp, vp, vp, vp]
         L.intattn_cache_read.argtypes = [vp, vp, scp, i32, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp]
+        L.intattn_decode_shared_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        L.intattn_decode_shared_workspace_size.restype = ctypes.c_size_t
+        L.intattn_decode_shared.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, scp, i32, i32, i32, i32, i32, f32, i32,
+                                            vp, vp, ctypes.c_size_t, vp]
         L.intattn_gelu_derive_params.argtypes = [f32, f32, f32, ctypes.POINTER(_GeluParams)]
         L.intattn_gelu.argtypes = [vp, vp, ctypes.c_longlong, f32, f32, f32, vp]
         L.intattn_selftest_timeout.argtypes = [vp]
@@ -751,6 +756,65 @@ def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bi
     del keep
     _check(rc, "intattn_cache_read")
     return k_out, v_out
+
+
+def decode_shared_workspace_size(B: int, H: int, Hkv: int, Lmax: int, d: int) -> int:
+    return int(lib().intattn_decode_shared_workspace_size(int(B), int(H), int(Hkv), int(Lmax), int(d)))
+
+
+def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lengths, scales: Scales, clip_c: float, prefix_len=None,
+                  dtype=None, out=None, workspace=None, stream=None):
+    """out [B, H, 1, d]: one query per (b, h) over the first prefix_len rows
+    (None: all) of k_prefix, v_prefix [Hkv, Lp, d], shared by the batch, and
+    then the first lengths[b] rows (int32 CUDA [B]; None: all) of k_cache,
+    v_cache [B, Hkv, Lmax, d].  H a multiple of Hkv; scales.s_q, s_o, clip: H
+    entries per head, s_k, s_v, z_k, z_v: Hkv.  dtype: torch.int8 (default),
+    the codes; float16 / bfloat16, the values they stand for."""
+    import torch
+    _check_tensor(q, "q")
+    dev = q.device
+    if q.dim() != 4 or q.shape[2] != 1:
+        raise ValueError("decode_shared takes one query per (b, h): q is [B, H, 1, d]")
+    B, H, _, d = q.shape
+    for t, n, z in ((k_prefix, "k_prefix", scales.z_k), (v_prefix, "v_prefix", scales.z_v),
+                    (k_cache, "k_cache", scales.z_k), (v_cache, "v_cache", scales.z_v)):
+        _check_codes(t, n, z)
+        if t.device != dev:
+            raise ValueError(f"{n} must be on {dev}")
+    if k_cache.dim() != 4 or k_prefix.dim() != 3:
+        raise ValueError("prefixes are [Hkv, Lp, d], caches [B, Hkv, Lmax, d]")
+    Hkv, Lmax = k_cache.shape[1:3]
+    if k_cache.shape != (B, Hkv, Lmax, d) or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [B, Hkv, Lmax, d] matching q")
+    Lp_max = k_prefix.shape[1]
+    if k_prefix.shape != (Hkv, Lp_max, d) or v_prefix.shape != k_prefix.shape:
+        raise ValueError("prefixes must be [Hkv, Lp, d] matching the caches")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("the query heads must be a multiple of the K / V heads")
+    Lp = Lp_max if prefix_len is None else int(prefix_len)
+    _check_entries(scales, H, Hkv, ("s_q", "s_k", "s_v", "s_o", "clip", "z_k", "z_v"))
+    lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
+    dt = dtype or (out.dtype if out is not None else torch.int8)
+    kinds = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16, torch.int8: DTYPE_INT8}
+    if dt not in kinds:
+        raise TypeError("dtype must be int8, float16 or bfloat16")
+    sc, keep = scales._c()
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((B, H, 1, d), dtype=dt, device=dev)
+        if not isinstance(out, torch.Tensor) or out.dtype != dt or out.device != dev:
+            raise TypeError(f"out must be a {dt} tensor on {dev}")
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous and match q")
+        if workspace is None:
+            workspace = torch.empty(max(decode_shared_workspace_size(B, H, Hkv, Lmax, d), 1), dtype=torch.uint8, device=dev)
+        rc = lib().intattn_decode_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), Lp, Lp_max,
+                                         k_cache.data_ptr(), v_cache.data_ptr(), lp, sc, B, H, Hkv, Lmax, d,
+                                         float(clip_c), kinds[dt], out.data_ptr(), workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), st)
+    del keep
+    _check(rc, "intattn_decode_shared")
+    return out
 
 
 def gelu_params(s_x: float, s_y: float, c: float):

@@ -26,6 +26,7 @@
 #include "prefill_kernel.cuh"
 #include "prefill_short_kernel.cuh"
 #include "rows_kernel.cuh"
+#include "shared_kernel.cuh"
 
 using intattn::DecodeArgs;
 using intattn::HeadParamsDev;
@@ -964,6 +965,7 @@ int quantize_impl(const void* x, int dtype, int B, int H, int L, int d, int per_
 }  // namespace
 
 #include "rows_api.cuh"
+#include "shared_api.cuh"
 
 extern "C" {
 
