@@ -28,7 +28,76 @@ int shared_params(const intattn_scales_t* sc, int H, int Hkv, int d, float clip_
   x.s_v = s_v;
   x.z_k = sc->z_k ? z_k : nullptr;
   x.z_v = sc->z_v ? z_v : nullptr;
-  return derive(&x, H, d, clip_c, a->lut, a->hp, INTATTN_MAX_HEADS);
+  return derive(&x, H, d, clip_c, a->lut, a->hp, INTATTN_MAX_HEADS, &a->n_luts);
+}
+
+struct SharedLayout {
+  int ld_s;
+  size_t zeroed;  // words the zero kernel clears: counters and row maxima
+  size_t off_z, off_p, off_acc, off_s, total;
+};
+
+SharedLayout shared_layout(long long BH, int Lmax, int d) {
+  SharedLayout L{};
+  const size_t rows = static_cast<size_t>(BH);
+  L.zeroed = 8 + rows;
+  L.off_z = round256(4 * L.zeroed);
+  // row_z, row_p and acc are consecutive (cleared together by the kernel);
+  // acc starts on 16 bytes
+  L.off_acc = (L.off_z + 8 * rows + 15) & ~size_t(15);
+  L.off_z = L.off_acc - 8 * rows;
+  L.off_p = L.off_z + 4 * rows;
+  L.ld_s = (Lmax + 3) & ~3;
+  L.off_s = round256(L.off_acc + 4 * rows * d);
+  L.total = L.off_s + round256(4 * rows * static_cast<size_t>(L.ld_s));
+  return L;
+}
+
+template <int D>
+int shared_launch(const SharedArgs& a, int grid, const SharedLayout& L, cudaStream_t st) {
+  using C = intattn::shared::Cfg<D>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return INTATTN_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(intattn::shared::shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(C::kSmemBytes)) != cudaSuccess)
+      return note_launch(cudaGetLastError());
+    attr_set[dev] = true;
+  }
+  const int n = static_cast<int>(L.zeroed);
+  intattn::shared::shared_zero_kernel<<<std::min(32, (n + 255) / 256), 256, 0, st>>>(a.ctr, n);
+  const int rc = note_launch(cudaGetLastError());
+  if (rc) return rc;
+  // cooperative: all CTAs resident (the grid barriers); programmatic
+  // serialisation: set-up and the first loads overlap the zero kernel
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeCooperative;
+  attrs[0].val.cooperative = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(intattn::shared::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
+  return note_launch(cudaLaunchKernelEx(&cfg, intattn::shared::shared_kernel<D>, a));
+}
+
+// [Hkv, rows of Lp_max, d] with the first Lp rows visible (rows past them
+// read as 0), box {d, 128, 1}.
+bool encode_prefix(CUtensorMap* m, const void* base, int d, int Lp, int Lp_max, int Hkv) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Lp), static_cast<cuuint64_t>(Hkv)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Lp_max) * d};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), intattn::shared::kBN, 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -37,7 +106,7 @@ extern "C" {
 
 size_t intattn_decode_shared_workspace_size(int B, int H, int Hkv, int Lmax, int d) {
   if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv || Lmax < 0 || (d != 64 && d != 128)) return 0;
-  return 256;
+  return shared_layout(static_cast<long long>(B) * H, Lmax, d).total;
 }
 
 int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t* v_prefix, int Lp, int Lp_max,
@@ -66,30 +135,46 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   if (!workspace || workspace_bytes < intattn_decode_shared_workspace_size(B, H, Hkv, Lmax, d) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return INTATTN_ERR_WORKSPACE;
+  const SharedLayout L = shared_layout(BH, Lmax, d);
+  char* ws = static_cast<char*>(workspace);
   a.q = q;
-  a.kp = k_prefix;
-  a.vp = v_prefix;
   a.kc = k_cache;
   a.vc = v_cache;
   a.lengths = lengths;
   a.out = out;
+  a.ctr = reinterpret_cast<uint32_t*>(ws);
+  a.row_max = a.ctr + 8;
+  a.row_z = reinterpret_cast<int32_t*>(ws + L.off_z);
+  a.row_p = reinterpret_cast<int32_t*>(ws + L.off_p);
+  a.acc = reinterpret_cast<float*>(ws + L.off_acc);
+  a.scores = reinterpret_cast<int32_t*>(ws + L.off_s);
+  a.ld_s = L.ld_s;
   a.B = B;
   a.H = H;
   a.Hkv = Hkv;
   a.G = H / Hkv;
+  a.R = B * a.G;
   a.Lp = Lp;
-  a.Lp_max = Lp_max;
   a.Lmax = Lmax;
+  a.key_tiles = (Lp + intattn::shared::kBN - 1) / intattn::shared::kBN;
+  a.row_tiles = (a.R + intattn::shared::kBM - 1) / intattn::shared::kBM;
   a.per_head = scales->per_head ? 1 : 0;
   a.out_kind = out_dtype;
   a.k_u8 = scales->z_k ? 1 : 0;
   a.v_u8 = scales->z_v ? 1 : 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (d == 64)
-    intattn::shared::shared_simple_kernel<64><<<static_cast<unsigned>(BH), intattn::shared::kThreads, 0, st>>>(a);
-  else
-    intattn::shared::shared_simple_kernel<128><<<static_cast<unsigned>(BH), intattn::shared::kThreads, 0, st>>>(a);
-  return note_launch(cudaGetLastError());
+  const long long tiles = static_cast<long long>(Hkv) * a.row_tiles * a.key_tiles;
+  if (tiles > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
+  a.tiles = static_cast<int32_t>(tiles);
+  if (Lp > 0 && (!encode_prefix(&a.tm_k, k_prefix, d, Lp, Lp_max, Hkv) ||
+                 !encode_prefix(&a.tm_v, v_prefix, d, Lp, Lp_max, Hkv)))
+    return INTATTN_ERR_CUDA;
+  int sms = 0;
+  if (sm_count(&sms) != INTATTN_OK) return INTATTN_ERR_CUDA;
+  // as many CTAs as there are prefix tiles or 128-key pieces of own rows
+  const long long own = static_cast<long long>(B) * Hkv * ((Lmax + 127) / 128);
+  const int grid = static_cast<int>(std::min<long long>(sms, std::max<long long>(std::max(tiles, own), 1)));
+  return d == 64 ? shared_launch<64>(a, grid, L, st) : shared_launch<128>(a, grid, L, st);
 }
 
 }  // extern "C"
