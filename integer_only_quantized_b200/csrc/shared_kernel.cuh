@@ -25,12 +25,14 @@
 // a range within one (head, row tile) is a segment.
 //
 // Own rows.  They are read by one sequence only: an HBM stream with up to
-// eight query rows per K / V row.  The softmax warps take 16 or 128 keys at a
-// time with 16- and 8-byte loads straight to registers, one item ahead, and
-// m16n8k32 integer MMAs (keys or channels on the 16 side, the G grouped heads
-// on the 8 side): the contraction order is free, so each thread's contiguous
-// bytes serve as its fragment and K needs no shuffling.  Their scores (4
-// bytes per key and head) wait in the workspace.
+// eight query rows per K / V row.  Each softmax warp takes an equal
+// consecutive share of all blocks of own rows and streams it through a ring
+// of its own (two 2 KB TMA tiles, in the memory of the tables, which those
+// parts of the phases do not use): 64 KB in flight per SM without registers
+// or barriers shared by warps.  The products are m16n8k32 integer MMAs, keys or
+// channels on the 16 side and the grouped heads on the 8 side; the contraction order
+// is free, so a thread's 16 consecutive bytes of K serve as its fragments.
+// Scores (4 bytes per key and head) wait in the workspace.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -50,9 +52,8 @@ namespace intattn {
 
 struct SharedArgs {
   CUtensorMap tm_k, tm_v;     // prefix [Hkv, Lp, d], box {d, 128, 1}
+  CUtensorMap tm_kc, tm_vc;   // own rows [B Hkv, Lmax, d], boxes {d, 2048 / d, 1} and {64, 32, 1}
   const int8_t* q;            // [B, H, d]
-  const int8_t* kc;           // [B, Hkv, Lmax, d] each sequence's own rows
-  const int8_t* vc;
   const int32_t* lengths;     // [B], or null: Lmax
   void* out;                  // [B, H, d] int8 codes, or fp16 / bf16 values
   // workspace; row r of K / V head hk (r = b G + g) is row hk R + r
@@ -110,7 +111,8 @@ enum Bar : int {
   kBarOFull = 16,
   kBarOEmpty = 17,
   kBarDrain = 18,
-  kBarKvFull = 19,  // [stages], then kv_empty[stages]
+  kBarOwn = 19,     // [16][2] tiles of the softmax warps' own rings
+  kBarKvFull = 51,  // [stages], then kv_empty[stages]
 };
 
 template <int D>
@@ -132,6 +134,7 @@ struct Cfg {
   static constexpr uint32_t kOffBars = kOffHp + INTATTN_MAX_HEADS * sizeof(HeadParamsDev);
   static constexpr uint32_t kOffMisc = kOffBars + kNumBars * 8;  // TMEM address, barrier verdict
   static constexpr uint32_t kUsed = kOffMisc + 16;
+  static_assert(4 * kTabBytes >= kSoftWarps * 4096 && kOffTab % 1024 == 0, "own rings in the tables' memory");
   // one CTA per SM: every CTA takes all 512 TMEM columns
   static constexpr uint32_t kSmemBytes = (kUsed + 1024 > 120 * 1024) ? kUsed + 1024 : 120 * 1024;
 };
@@ -183,100 +186,224 @@ __device__ __forceinline__ int own_rows(const SharedArgs& a, int b) {
   return n < 0 || n > a.Lmax ? 0 : n;
 }
 
-// A group of up to eight query rows of one (sequence, K / V head).
-struct Unit {
-  int b, hk, g0, rows, len;
-};
-__device__ __forceinline__ Unit unit_at(const SharedArgs& a, int u) {
-  Unit x;
-  const int groups = (a.G + 7) / 8;
-  const int bh = u / groups;
-  x.g0 = 8 * (u - bh * groups);
-  x.rows = min(8, a.G - x.g0);
-  x.b = bh / a.Hkv;
-  x.hk = bh - x.b * a.Hkv;
-  x.len = own_rows(a, x.b);
-  return x;
+// Blocks of `keys` keys over the own rows of every sequence and `units`
+// units per sequence, in the order (b, unit, block): their number, and the
+// block at position p.  Warp-collective.
+__device__ __forceinline__ long long own_blocks(const SharedArgs& a, int keys, int units) {
+  const int lane = threadIdx.x & 31;
+  long long n = 0;
+  for (int b = lane; b < a.B; b += 32) n += (own_rows(a, b) + keys - 1) / keys;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n * units;
 }
 
-// ---- phase A of the own rows: scores and row max, 16 keys per item ----
+struct Walk {
+  int b, u, blk, nb;  // nb: blocks of sequence b
+  __device__ __forceinline__ void seek(const SharedArgs& a, int keys, int units, long long p) {
+    const int lane = threadIdx.x & 31;
+    b = u = blk = nb = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int mine = b0 + lane < a.B ? (own_rows(a, b0 + lane) + keys - 1) / keys : 0;
+      long long incl = static_cast<long long>(mine) * units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > p);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        nb = __shfl_sync(0xffffffffu, mine, l);
+        p -= __shfl_sync(0xffffffffu, incl, l) - static_cast<long long>(nb) * units;
+        b = b0 + l;
+        u = static_cast<int>(p / nb);
+        blk = static_cast<int>(p - static_cast<long long>(u) * nb);
+        return;
+      }
+      p -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  // to the next block (there is one); true if the unit changed
+  __device__ __forceinline__ bool next(const SharedArgs& a, int keys, int units) {
+    if (++blk < nb) return false;
+    blk = 0;
+    if (++u == units) {
+      u = 0;
+      do {
+        ++b;
+        nb = (own_rows(a, b) + keys - 1) / keys;
+      } while (nb == 0);
+    }
+    return true;
+  }
+};
+
+// A warp's private ring of two 2 KB slots for the own rows' tiles: lane 0
+// issues the loads, every lane waits.
+struct OwnRing {
+  uint32_t base, bar;  // shared addresses: slot i at base + 2048 i, barrier i at bar + 8 i
+  uint32_t issued, used;
+  __device__ __forceinline__ void issue(const CUtensorMap* tm, int x, int y, int z) {
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t i = issued & 1;
+      mbar_arrive_expect_tx(bar + 8 * i, 2048);
+      tma_load_3d(base + 2048 * i, tm, bar + 8 * i, x, y, z);
+    }
+    ++issued;
+  }
+  // the oldest tile not yet used (its address), or 0 when the wait ran out
+  __device__ __forceinline__ uint32_t wait(unsigned role) {
+    const uint32_t i = used & 1, par = (used >> 1) & 1;
+    ++used;
+    if (mbar_wait_warp(bar + 8 * i, par, role)) return base + 2048 * i;
+    if (used < issued) {  // give up, but leave no copy in flight
+      mbar_wait_warp(bar + 8 * (used & 1), (used >> 1) & 1, role);
+      ++used;
+    }
+    return 0u;
+  }
+};
+
+__device__ __forceinline__ uint4 lds_u128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds_u64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Where the score of key kk of a 32-key block is kept: thread t of phase C
+// reads the four scores of a word with one load (position 16 g + 4 t + i) and
+// the V bytes of their keys from rows whose 16-byte pieces lie in other
+// banks than those of the other threads' rows (see own_pv).
+__device__ __forceinline__ int score_at(int kk) {
+  return (kk & 16) | ((kk & 4) << 1) | ((kk & 1) << 2) | ((kk & 8) >> 2) | ((kk & 2) >> 1);
+}
+__device__ __forceinline__ int key_of(int t, int i) {  // word 4 g + .. of thread t: i = 0 .. 7
+  return (t & 1) + 4 * (t >> 1) + 2 * (i & 1) + 8 * ((i >> 1) & 1) + 16 * (i >> 2);
+}
+
+// ---- phase A of the own rows: scores and row max ----
+// Units (hk, group of eight query heads).  A key past the sequence's last
+// (in its last 32-key block) gets the lowest score, whose table entry is 0.
 template <int D, bool kKSigned>
-__device__ __forceinline__ void own_scores(const SharedArgs& a, int warp, int warps, int longest) {
-  constexpr int kCh = D / 64;  // 16-byte pieces of a row per thread: piece t (and t + 4)
+__device__ __forceinline__ bool own_scores(const SharedArgs& a, OwnRing& ring, int warp, int warps) {
+  constexpr int kKeys = 2048 / D;      // 16 or 32
+  constexpr int kSub = kKeys / 16;     // 16-key products per block
+  constexpr int kCh = D / 64;          // 16-byte pieces of a row per thread: piece t (and t + 4)
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
-  const int units = a.B * a.Hkv * ((a.G + 7) / 8);
-  const int blocks = (longest + 15) / 16;
-  const long long items = static_cast<long long>(units) * blocks;
-  struct Item {
-    uint4 k[2][kCh], q[kCh];
+  const int groups = (a.G + 7) / 8, units = a.Hkv * groups;
+  const long long total = own_blocks(a, kKeys, units);
+  const long long lo = total * warp / warps, hi = total * (warp + 1) / warps;
+  const int n = static_cast<int>(hi - lo);
+  if (n == 0) return true;
+  Walk ld, w;
+  w.seek(a, kKeys, units, lo);
+  ld = w;
+  auto issue = [&]() { ring.issue(&a.tm_kc, 0, ld.blk * kKeys, ld.b * a.Hkv + ld.u / groups); };
+  issue();
+  if (n > 1) {
+    ld.next(a, kKeys, units);
+    issue();
+  }
+  uint4 q[kCh];
+  int hk = 0, rows = 0, len = 0;
+  size_t at = 0;       // first query row of the unit, in the row arrays
+  int32_t* sp = nullptr;
+  int32_t m[2];
+  auto enter = [&]() {
+    hk = w.u / groups;
+    const int g0 = 8 * (w.u - hk * groups);
+    rows = min(8, a.G - g0);
+    len = own_rows(a, w.b);
+    at = static_cast<size_t>(hk) * a.R + w.b * a.G + g0;
+    const size_t head = static_cast<size_t>(w.b) * a.H + hk * a.G + g0;
+    sp = a.scores + (head + 2 * t) * a.ld_s;
+#pragma unroll
+    for (int c = 0; c < kCh; ++c)
+      q[c] = n8 < rows ? __ldg(reinterpret_cast<const uint4*>(a.q + (head + n8) * D + 16 * t + 64 * c))
+                       : make_uint4(0, 0, 0, 0);
+    m[0] = m[1] = INT_MIN;
   };
-  auto fetch = [&](long long it, Item& f) {
-    const int blk = static_cast<int>(it / units);
-    const Unit x = unit_at(a, static_cast<int>(it - static_cast<long long>(blk) * units));
-    if (16 * blk >= x.len) return;
-    const int8_t* kb = a.kc + ((static_cast<size_t>(x.b) * a.Hkv + x.hk) * a.Lmax) * D + 16 * t;
-    const int8_t* qb = a.q + (static_cast<size_t>(x.b) * a.H + x.hk * a.G + x.g0 + n8) * D + 16 * t;
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = 16 * blk + 8 * i + n8;
-        f.k[i][c] = j < x.len ? decode::ld_stream(kb + static_cast<size_t>(j) * D + 64 * c) : make_uint4(0, 0, 0, 0);
-      }
-      f.q[c] = n8 < x.rows ? __ldg(reinterpret_cast<const uint4*>(qb + 64 * c)) : make_uint4(0, 0, 0, 0);
-    }
-  };
-  auto work = [&](long long it, const Item& f) {
-    const int blk = static_cast<int>(it / units);
-    const Unit x = unit_at(a, static_cast<int>(it - static_cast<long long>(blk) * units));
-    if (16 * blk >= x.len) return;
-    int32_t s[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) {
-      const uint4 k0 = f.k[0][c], k1 = f.k[1][c], q = f.q[c];
-      mma16832<kKSigned, true>(s, k0.x, k1.x, k0.y, k1.y, q.x, q.y);
-      mma16832<kKSigned, true>(s, k0.z, k1.z, k0.w, k1.w, q.z, q.w);
-    }
-    // s[0], s[1]: key n8, rows 2t and 2t + 1; s[2], s[3]: key n8 + 8
-    int32_t* sp = a.scores + (static_cast<size_t>(x.b) * a.H + x.hk * a.G + x.g0 + 2 * t) * a.ld_s + 16 * blk + n8;
-    int32_t m[2] = {INT_MIN, INT_MIN};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (16 * blk + 8 * i + n8 >= x.len) continue;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (2 * t + r < x.rows) sp[static_cast<size_t>(r) * a.ld_s + 8 * i] = s[2 * i + r];
-        m[r] = imax(m[r], s[2 * i + r]);
-      }
-    }
+  auto leave = [&]() {
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       m[0] = imax(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
       m[1] = imax(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
     }
-    if (n8 < 2 && 2 * t + n8 < x.rows)
-      atomicMax(a.row_max + static_cast<size_t>(x.hk) * a.R + x.b * a.G + x.g0 + 2 * t + n8, bias(n8 ? m[1] : m[0]));
+    if (n8 < 2 && 2 * t + n8 < rows) atomicMax(a.row_max + at + 2 * t + n8, bias(n8 ? m[1] : m[0]));
   };
-  Item f[2];
-  long long it = warp;
-  if (it < items) fetch(it, f[0]);
-  for (; it < items; it += 2ll * warps) {
-    if (it + warps < items) fetch(it + warps, f[1]);
-    work(it, f[0]);
-    if (it + warps >= items) break;
-    if (it + 2ll * warps < items) fetch(it + 2ll * warps, f[0]);
-    work(it + warps, f[1]);
+  enter();
+  for (int i = 0; i < n; ++i) {
+    const uint32_t tile = ring.wait(kRoleSoftmax);
+    if (tile == 0) return false;
+    uint4 k[kSub][2][kCh];
+#pragma unroll
+    for (int s = 0; s < kSub; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) {
+          const int row = 16 * s + 8 * e + n8;  // the TMA's swizzle on the 16-byte piece
+          const int piece = D == 128 ? ((t + 4 * c) ^ (row & 7)) : (t ^ ((row >> 1) & 3));
+          k[s][e][c] = lds_u128(tile + row * D + 16 * piece);
+        }
+    __syncwarp();  // every lane has read the tile
+    if (i + 2 < n) {
+      ld.next(a, kKeys, units);
+      issue();
+    }
+#pragma unroll
+    for (int s = 0; s < kSub; ++s) {
+      int32_t d[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < kCh; ++c) {
+        mma16832<kKSigned, true>(d, k[s][0][c].x, k[s][1][c].x, k[s][0][c].y, k[s][1][c].y, q[c].x, q[c].y);
+        mma16832<kKSigned, true>(d, k[s][0][c].z, k[s][1][c].z, k[s][0][c].w, k[s][1][c].w, q[c].z, q[c].w);
+      }
+      // d[0], d[1]: key n8, rows 2t and 2t + 1; d[2], d[3]: key n8 + 8
+      const int j0 = w.blk * kKeys + 16 * s;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = j0 + 8 * e + n8;
+        int32_t* dst = sp + (j & ~31) + score_at(j & 31);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int32_t v = j < len ? d[2 * e + r] : INT_MIN;
+          if (2 * t + r < rows) {
+            dst[static_cast<size_t>(r) * a.ld_s] = v;
+            // the second half of a last 32-key block that no tile covers
+            if (kKeys == 16 && (j0 & 16) == 0 && j0 + 16 >= len)
+              (dst + 16)[static_cast<size_t>(r) * a.ld_s] = INT_MIN;
+          }
+          m[r] = imax(m[r], v);
+        }
+      }
+    }
+    if (i + 1 < n && w.blk + 1 == w.nb) {
+      leave();
+      w.next(a, kKeys, units);
+      enter();
+    } else if (i + 1 < n) {
+      w.next(a, kKeys, units);
+    }
   }
+  leave();
+  return true;
 }
 
 // Index arithmetic of one row on the integer pipe (as decode_kernel.cuh):
-// idx = (Cm - max(S, lo) M) >> s in wrapping 32-bit arithmetic.
+// idx = (Cm - max(S, lo) M) >> s in wrapping 32-bit arithmetic.  lo = m - D
+// stays above the lowest int: D < 61 2^25 and |m| < 2^23.
 struct RowIndex {
   int32_t lo;
   uint32_t M, s, Cm;
-  __device__ __forceinline__ RowIndex(const HeadParamsDev& hp, int32_t m) {
-    const long long lo64 = static_cast<long long>(m) - hp.D;
-    lo = lo64 < INT_MIN ? INT_MIN : static_cast<int32_t>(lo64);
+  __device__ __forceinline__ void set(const HeadParamsDev& hp, int32_t m) {
+    lo = m - hp.D;
     M = static_cast<uint32_t>(hp.M);
     s = static_cast<uint32_t>(hp.s);
     Cm = static_cast<uint32_t>(m) * M + (1u << (s - 1));
@@ -286,139 +413,190 @@ struct RowIndex {
   }
 };
 
-// ---- phase B of the own rows: Z, 128 keys of one query row per item ----
+// ---- phase B of the own rows: Z, 128 scores of one query row per block ----
 __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDev* hp_s, const uint32_t* lut_s, int warp,
-                                         int warps, int longest) {
+                                         int warps) {
   const int lane = threadIdx.x & 31;
-  const int rows = a.B * a.H;
-  const int blocks = (longest + 127) / 128;
-  const long long items = static_cast<long long>(rows) * blocks;
-  for (long long it = warp; it < items; it += warps) {
-    const int blk = static_cast<int>(it / rows);
-    const int row = static_cast<int>(it - static_cast<long long>(blk) * rows);
-    const int b = row / a.H, h = row - b * a.H, hk = h / a.G;
-    const int len = own_rows(a, b);
-    if (128 * blk >= len) continue;
-    const size_t at = static_cast<size_t>(hk) * a.R + b * a.G + (h - hk * a.G);
-    const HeadParamsDev hp = hp_s[a.per_head ? h : 0];
-    const RowIndex index(hp, unbias(__ldcg(a.row_max + at)));
-    const uint32_t* lut = lut_s + 32 * hp.lut;
-    const int j = 128 * blk + 4 * lane;
-    uint32_t z = 0;
-    if (j < len) {
-      const int4 s = __ldcg(reinterpret_cast<const int4*>(a.scores + static_cast<size_t>(row) * a.ld_s + j));
-      z = lut[index(s.x)];
-      if (j + 1 < len) z += lut[index(s.y)];
-      if (j + 2 < len) z += lut[index(s.z)];
-      if (j + 3 < len) z += lut[index(s.w)];
-    }
+  const long long total = own_blocks(a, 128, a.H);
+  const long long lo = total * warp / warps, hi = total * (warp + 1) / warps;
+  const int n = static_cast<int>(hi - lo);
+  if (n == 0) return;
+  Walk w;
+  w.seek(a, 128, a.H, lo);
+  size_t at = 0;
+  int rounded = 0;
+  const int32_t* sp = nullptr;
+  const uint32_t* lut = nullptr;
+  RowIndex index;
+  uint32_t z = 0;
+  auto enter = [&]() {
+    const int hk = w.u / a.G;
+    at = static_cast<size_t>(hk) * a.R + w.b * a.G + (w.u - hk * a.G);
+    const HeadParamsDev hp = hp_s[a.per_head ? w.u : 0];
+    index.set(hp, unbias(__ldcg(a.row_max + at)));
+    lut = lut_s + 32 * hp.lut;
+    sp = a.scores + (static_cast<size_t>(w.b) * a.H + w.u) * a.ld_s + 4 * lane;
+    rounded = (own_rows(a, w.b) + 31) & ~31;  // every score of a started 32-key block is set
+    z = 0;
+  };
+  auto leave = [&]() {
     z = __reduce_add_sync(0xffffffffu, z);
     if (lane == 0) atomicAdd(a.row_z + at, static_cast<int32_t>(z));
+  };
+  enter();
+  for (int i = 0; i < n; ++i) {
+    if (128 * w.blk + 4 * lane < rounded) {
+      const int4 s = __ldcg(reinterpret_cast<const int4*>(sp + 128 * w.blk));
+      z += (lut[index(s.x)] + lut[index(s.y)]) + (lut[index(s.z)] + lut[index(s.w)]);
+    }
+    if (i + 1 < n && w.blk + 1 == w.nb) {
+      leave();
+      w.next(a, 128, a.H);
+      enter();
+    } else if (i + 1 < n) {
+      w.next(a, 128, a.H);
+    }
   }
+  leave();
 }
 
-// ---- phase C of the own rows: P.V over 128 keys and 64 channels per item ----
+// ---- phase C of the own rows: P.V, 32 keys and 64 channels per block ----
+// Units (hk, group of eight query heads, half of the channels).  A = V^T: the
+// thread (n8, t) reads eight channels (8 n8 ..) of the eight keys key_of(t, i);
+// four keys of a channel make a fragment word.  B = P: query row n8, the
+// same keys.
 template <int D, bool kVSigned>
-__device__ __forceinline__ void own_pv(const SharedArgs& a, const HeadParamsDev* hp_s, const uint32_t* lut_s, int warp,
-                                       int warps, int longest) {
+__device__ __forceinline__ bool own_pv(const SharedArgs& a, OwnRing& ring, const HeadParamsDev* hp_s,
+                                       const uint32_t* lut_s, int warp, int warps) {
   constexpr int kHalves = D / 64;
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
-  const int units = a.B * a.Hkv * ((a.G + 7) / 8) * kHalves;
-  const int blocks = (longest + 127) / 128;
-  const long long items = static_cast<long long>(units) * blocks;
-  for (long long it = warp; it < items; it += warps) {
-    const int blk = static_cast<int>(it / units);
-    const int uh = static_cast<int>(it - static_cast<long long>(blk) * units);
-    const Unit x = unit_at(a, uh / kHalves);
-    const int dh = uh % kHalves;
-    const int j0 = 128 * blk, j1 = min(x.len, j0 + 128);
-    if (j0 >= j1) continue;
-    // V bytes of channels 64 dh + 8 n8 .. + 7 and keys 4t .. 4t + 3, 16 + 4t .. of a 32-key step
-    const int8_t* vb = a.vc + ((static_cast<size_t>(x.b) * a.Hkv + x.hk) * a.Lmax) * D + 64 * dh + 8 * n8;
-    auto load = [&](int step, uint2 (&v)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = j0 + 32 * step + (i < 4 ? 4 * t + i : 12 + 4 * t + i);
-        v[i] = j < j1 ? decode::ld_stream8(vb + static_cast<size_t>(j) * D) : make_uint2(0, 0);
-      }
-    };
-    uint2 cur[8], nxt[8];
-    load(0, cur);
-    // the u8 probabilities of query row n8: word 2 i (+1) holds keys 4t (16 + 4t) .. + 3 of step i
-    uint32_t p[8];
-    int32_t psum = 0;
-    const size_t at = static_cast<size_t>(x.hk) * a.R + x.b * a.G + x.g0 + n8;
-    if (n8 < x.rows) {
-      const int h = x.hk * a.G + x.g0 + n8;
-      const HeadParamsDev hp = hp_s[a.per_head ? h : 0];
-      const RowIndex index(hp, unbias(__ldcg(a.row_max + at)));
-      const unsigned long long R = exact_R(__ldcg(a.row_z + at));
-      const uint32_t* lut = lut_s + 32 * hp.lut;
-      const int32_t* sp = a.scores + (static_cast<size_t>(x.b) * a.H + h) * a.ld_s + j0;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const int j = 32 * (w >> 1) + 16 * (w & 1) + 4 * t;
-        p[w] = 0;
-        if (j0 + j < j1) {
-          const int4 s4 = __ldcg(reinterpret_cast<const int4*>(sp + j));
-          const int32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (j0 + j + i < j1)
-              p[w] |= static_cast<uint32_t>((lut[index(s[i])] * R + (1ull << 31)) >> 32) << (8 * i);
-          }
-        }
-        psum = static_cast<int32_t>(__dp4a(p[w], 0x01010101u, static_cast<uint32_t>(psum)));
-      }
-      if (a.v_u8 && dh == 0 && psum != 0) atomicAdd(a.row_p + at, psum);
-    } else {
-#pragma unroll
-      for (int w = 0; w < 8; ++w) p[w] = 0;
-    }
-    int32_t o[4][4];
+  const int groups = (a.G + 7) / 8, units = a.Hkv * groups * kHalves;
+  const long long total = own_blocks(a, 32, units);
+  const long long lo = total * warp / warps, hi = total * (warp + 1) / warps;
+  const int n = static_cast<int>(hi - lo);
+  if (n == 0) return true;
+  Walk ld, w;
+  w.seek(a, 32, units, lo);
+  ld = w;
+  auto issue = [&]() {
+    ring.issue(&a.tm_vc, 64 * (ld.u % kHalves), 32 * ld.blk, ld.b * a.Hkv + ld.u / (groups * kHalves));
+  };
+  issue();
+  if (n > 1) {
+    ld.next(a, 32, units);
+    issue();
+  }
+  size_t at = 0;
+  int rows = 0, dh = 0;
+  const int32_t* sp = nullptr;
+  const uint32_t* lut = nullptr;
+  RowIndex index;
+  unsigned long long R = 0;
+  int32_t psum = 0;
+  int32_t o[4][4];
+  int4 s0, s1;
+  auto enter = [&]() {
+    dh = w.u % kHalves;
+    const int u = w.u / kHalves, hk = u / groups, g0 = 8 * (u - hk * groups);
+    rows = min(8, a.G - g0);
+    at = static_cast<size_t>(hk) * a.R + w.b * a.G + g0;
+    const int h = hk * a.G + g0 + min(n8, rows - 1);
+    sp = a.scores + (static_cast<size_t>(w.b) * a.H + h) * a.ld_s + 4 * t;
+    const HeadParamsDev hp = hp_s[a.per_head ? h : 0];
+    const size_t mine = at + min(n8, rows - 1);
+    index.set(hp, unbias(__ldcg(a.row_max + mine)));
+    R = exact_R(__ldcg(a.row_z + mine));
+    lut = lut_s + 32 * hp.lut;
+    psum = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[c][i] = 0;
-#pragma unroll
-    for (int step = 0; step < 4; ++step) {
-      if (j0 + 32 * step < j1) {
-        if (step < 3 && j0 + 32 * (step + 1) < j1) load(step + 1, nxt);
-        // bytes (key i, channel c) -> word c holds four keys of channel c
-        uint32_t w[2][8];
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t r0 = half ? cur[4 * g].y : cur[4 * g].x, r1 = half ? cur[4 * g + 1].y : cur[4 * g + 1].x;
-            const uint32_t r2 = half ? cur[4 * g + 2].y : cur[4 * g + 2].x;
-            const uint32_t r3 = half ? cur[4 * g + 3].y : cur[4 * g + 3].x;
-            const uint32_t ab_lo = __byte_perm(r0, r1, 0x5140), ab_hi = __byte_perm(r0, r1, 0x7362);
-            const uint32_t cd_lo = __byte_perm(r2, r3, 0x5140), cd_hi = __byte_perm(r2, r3, 0x7362);
-            w[g][4 * half] = __byte_perm(ab_lo, cd_lo, 0x5410);
-            w[g][4 * half + 1] = __byte_perm(ab_lo, cd_lo, 0x7632);
-            w[g][4 * half + 2] = __byte_perm(ab_hi, cd_hi, 0x5410);
-            w[g][4 * half + 3] = __byte_perm(ab_hi, cd_hi, 0x7632);
-          }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          mma16832<kVSigned, false>(o[c], w[0][2 * c], w[0][2 * c + 1], w[1][2 * c], w[1][2 * c + 1], p[2 * step],
-                                    p[2 * step + 1]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
-      }
+  };
+  auto load_scores = [&]() {
+    s0 = __ldcg(reinterpret_cast<const int4*>(sp + 32 * w.blk));
+    s1 = __ldcg(reinterpret_cast<const int4*>(sp + 32 * w.blk + 16));
+  };
+  auto leave = [&]() {
+    if (a.v_u8 && dh == 0) {
+      psum += __shfl_xor_sync(0xffffffffu, psum, 1);
+      psum += __shfl_xor_sync(0xffffffffu, psum, 2);
+      if (t == 0 && n8 < rows) atomicAdd(a.row_p + at + n8, psum);
     }
     // o[c][0..1]: channel 8 n8 + 2c, rows 2t, 2t + 1; o[c][2..3]: channel 8 n8 + 2c + 1
 #pragma unroll
     for (int r = 0; r < 2; ++r)
-      if (2 * t + r < x.rows) {
-        float* dst = a.acc + (static_cast<size_t>(x.hk) * a.R + x.b * a.G + x.g0 + 2 * t + r) * D + 64 * dh + 8 * n8;
+      if (2 * t + r < rows) {
+        float* dst = a.acc + (at + 2 * t + r) * D + 64 * dh + 8 * n8;
         red_add4(dst, static_cast<float>(o[0][r]), static_cast<float>(o[0][2 + r]), static_cast<float>(o[1][r]),
                  static_cast<float>(o[1][2 + r]));
         red_add4(dst + 4, static_cast<float>(o[2][r]), static_cast<float>(o[2][2 + r]), static_cast<float>(o[3][r]),
                  static_cast<float>(o[3][2 + r]));
       }
+  };
+  enter();
+  load_scores();
+  for (int i = 0; i < n; ++i) {
+    // P of this block (0 for rows the unit does not have)
+    uint32_t p[2];
+    {
+      const int32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          b[e] = static_cast<uint32_t>((lut[index(s[4 * g + e])] * R + (1ull << 31)) >> 32);
+        p[g] = n8 < rows ? prefill::pack4(b[0], b[1], b[2], b[3]) : 0u;
+        psum = static_cast<int32_t>(__dp4a(p[g], 0x01010101u, static_cast<uint32_t>(psum)));
+      }
+    }
+    const bool last = i + 1 == n;
+    const bool moves = !last && w.blk + 1 == w.nb;  // the next block is another unit's
+    if (!last && !moves) {
+      w.next(a, 32, units);
+      load_scores();
+    }
+    const uint32_t tile = ring.wait(kRoleSoftmax);
+    if (tile == 0) return false;
+    uint2 v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int row = key_of(t, e);  // the TMA's 64-byte swizzle on the 16-byte piece
+      v[e] = lds_u64(tile + row * 64 + 16 * ((n8 >> 1) ^ ((row >> 1) & 3)) + 8 * (n8 & 1));
+    }
+    __syncwarp();
+    if (i + 2 < n) {
+      ld.next(a, 32, units);
+      issue();
+    }
+    // bytes (key, channel c) -> word c holds four keys of channel c
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t x[2][4];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint32_t r0 = half ? v[4 * g].y : v[4 * g].x, r1 = half ? v[4 * g + 1].y : v[4 * g + 1].x;
+        const uint32_t r2 = half ? v[4 * g + 2].y : v[4 * g + 2].x, r3 = half ? v[4 * g + 3].y : v[4 * g + 3].x;
+        const uint32_t ab_lo = __byte_perm(r0, r1, 0x5140), ab_hi = __byte_perm(r0, r1, 0x7362);
+        const uint32_t cd_lo = __byte_perm(r2, r3, 0x5140), cd_hi = __byte_perm(r2, r3, 0x7362);
+        x[g][0] = __byte_perm(ab_lo, cd_lo, 0x5410);
+        x[g][1] = __byte_perm(ab_lo, cd_lo, 0x7632);
+        x[g][2] = __byte_perm(ab_hi, cd_hi, 0x5410);
+        x[g][3] = __byte_perm(ab_hi, cd_hi, 0x7632);
+      }
+      mma16832<kVSigned, false>(o[2 * half], x[0][0], x[0][1], x[1][0], x[1][1], p[0], p[1]);
+      mma16832<kVSigned, false>(o[2 * half + 1], x[0][2], x[0][3], x[1][2], x[1][3], p[0], p[1]);
+    }
+    if (moves) {
+      leave();
+      w.next(a, 32, units);
+      enter();
+      load_scores();
+    }
   }
+  leave();
+  return true;
 }
 
 // Requantised outputs of all rows, four channels per thread.
@@ -496,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     mbar_init(bar(kBarOFull), 1);
     mbar_init(bar(kBarOEmpty), kEpiWarps);
     mbar_init(bar(kBarDrain), 1);
+    for (int i = 0; i < 2 * kSoftWarps; ++i) mbar_init(bar(kBarOwn + i), 1);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(bar_kv_full(i), 1);
       mbar_init(bar_kv_empty(i), 1);
@@ -524,26 +703,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t trow = tlane + half * kCols;
     const uint32_t prow = smem_u32(tab) + 4u * r;
-    // items of the own rows: neighbours in the order go to different CTAs
-    const int ow = sw * gridDim.x + blockIdx.x, ows = kSoftWarps * gridDim.x;
-    int longest = 0;
-    if (args.Lmax > 0) {
-      if (args.lengths == nullptr) {
-        longest = args.Lmax;
-      } else {
-        bool bad = false;
-        for (int b = lane; b < args.B; b += 32) {
-          const int n = __ldg(args.lengths + b);
-          bad |= n < 0 || n > args.Lmax;
-          longest = max(longest, own_rows(args, b));
-        }
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        if (bad && blockIdx.x == 0 && sw == 0) atomicOr(&g_device_error, kErrParamRange);
+    const int ow = sw * gridDim.x + blockIdx.x, ows = kSoftWarps * gridDim.x;  // share of the own rows
+    OwnRing ring{s_base + C::kOffTab + 4096u * sw, bar(kBarOwn + 2 * sw), 0u, 0u};
+    if (args.lengths != nullptr && blockIdx.x == 0 && sw == 0)
+      for (int b = lane; b < args.B; b += 32) {
+        const int n = __ldg(args.lengths + b);
+        if (n < 0 || n > args.Lmax) atomicOr(&g_device_error, kErrParamRange);
       }
-    } else if (args.lengths != nullptr && blockIdx.x == 0 && sw == 0) {
-      for (int b = lane; b < args.B; b += 32)
-        if (__ldg(args.lengths + b) != 0) atomicOr(&g_device_error, kErrParamRange);
-    }
     bool ok = true;
     uint32_t sc = 0;  // S tiles so far
     uint32_t pc = 0;  // P tiles so far
@@ -594,10 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     quant::griddep_wait();  // the counters and row maxima are zeroed
 
     // ---- phase A ----
-    if (longest > 0) {
-      if (args.k_u8) own_scores<D, false>(args, ow, ows, longest);
-      else own_scores<D, true>(args, ow, ows, longest);
-    }
+    if (args.Lmax > 0)
+      ok = args.k_u8 ? own_scores<D, false>(args, ring, ow, ows) : own_scores<D, true>(args, ring, ow, ows);
     for (int t = t0; t < t1 && ok;) {
       const Segment sg = segment_at(args, t, t1);
       int32_t m = INT_MIN;
@@ -661,9 +825,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 
     // ---- phase B ----
     if (ok) {
-      if (sw < 4)
-        for (int b = 0; b < 4; ++b) tab[b * (C::kTabBytes / 4) + r] = 0u;  // row 0 stays 0
-      if (longest > 0) own_sums(args, hp_s, lut_s, ow, ows, longest);
+      if (sw < 4) tab[r] = 0u;  // row 0: masked keys
+      if (args.Lmax > 0) own_sums(args, hp_s, lut_s, ow, ows);
       for (int t = t0; t < t1;) {
         const Segment sg = segment_at(args, t, t1);
         const size_t at = row_index(sg);
@@ -705,11 +868,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 
     // ---- phase C ----
     if (ok) {
-      if (longest > 0) {
-        if (args.v_u8) own_pv<D, false>(args, hp_s, lut_s, ow, ows, longest);
-        else own_pv<D, true>(args, hp_s, lut_s, ow, ows, longest);
+      if (args.Lmax > 0) {
+        fence_proxy_async_smem();  // the tables' last accesses, before the ring's tiles land there
+        ok = args.v_u8 ? own_pv<D, false>(args, ring, hp_s, lut_s, ow, ows)
+                       : own_pv<D, true>(args, ring, hp_s, lut_s, ow, ows);
+        ok = soft_sync(ok);  // every ring is done with the tables' memory
       }
-      for (int t = t0; t < t1;) {
+      if (sw < 4)
+        for (int b = 0; b < 4; ++b) tab[b * (C::kTabBytes / 4) + r] = 0u;
+      for (int t = t0; t < t1 && ok;) {
         const Segment sg = segment_at(args, t, t1);
         const size_t at = row_index(sg);
         const unsigned long long R = exact_R(__ldcg(args.row_z + at));
