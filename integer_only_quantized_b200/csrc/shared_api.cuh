@@ -34,7 +34,7 @@ int shared_params(const intattn_scales_t* sc, int H, int Hkv, int d, float clip_
 struct SharedLayout {
   int ld_s;
   size_t zeroed;  // words the zero kernel clears: counters and row maxima
-  size_t off_z, off_p, off_acc, off_s, total;
+  size_t off_z, off_p, off_acc, off_s, off_i, total;
 };
 
 SharedLayout shared_layout(long long BH, int Lmax, int d) {
@@ -49,7 +49,8 @@ SharedLayout shared_layout(long long BH, int Lmax, int d) {
   L.off_p = L.off_z + 4 * rows;
   L.ld_s = (Lmax + 31) & ~31;  // whole 32-key blocks
   L.off_s = round256(L.off_acc + 4 * rows * d);
-  L.total = L.off_s + round256(4 * rows * static_cast<size_t>(L.ld_s));
+  L.off_i = L.off_s + round256(4 * rows * static_cast<size_t>(L.ld_s));
+  L.total = L.off_i + round256(rows * static_cast<size_t>(L.ld_s));
   return L;
 }
 
@@ -147,6 +148,7 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   a.row_p = reinterpret_cast<int32_t*>(ws + L.off_p);
   a.acc = reinterpret_cast<float*>(ws + L.off_acc);
   a.scores = reinterpret_cast<int32_t*>(ws + L.off_s);
+  a.index = reinterpret_cast<uint32_t*>(ws + L.off_i);
   a.ld_s = L.ld_s;
   a.B = B;
   a.H = H;

@@ -32,7 +32,8 @@
 // or barriers shared by warps.  The products are m16n8k32 integer MMAs, keys or
 // channels on the 16 side and the grouped heads on the 8 side; the contraction order
 // is free, so a thread's 16 consecutive bytes of K serve as its fragments.
-// Scores (4 bytes per key and head) wait in the workspace.
+// Scores (4 bytes per key and head), and from phase B on their table indices
+// (one byte), wait in the workspace.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -63,6 +64,7 @@ struct SharedArgs {
   int32_t* row_p;             // [Hkv R] sum of P (V zero-points)
   float* acc;                 // [Hkv R, d] sum of P.V
   int32_t* scores;            // [B H, ld_s] scores of the own rows
+  uint32_t* index;            // [B H, ld_s / 4] their table indices, a byte each
   int32_t B, H, Hkv, G, R, Lp, Lmax, ld_s, per_head, out_kind, k_u8, v_u8, n_luts;
   int32_t key_tiles, row_tiles;  // 128-key tiles of the prefix, 128-row tiles of R
   int32_t tiles;                 // Hkv * row_tiles * key_tiles
@@ -87,7 +89,7 @@ constexpr int kTeamWarps = kSoftWarps / kTeams;
 constexpr int kCols = 64;                  // S columns per thread and tile (two halves)
 constexpr int kProducerWarp = 16;
 constexpr int kMmaWarp = 17;
-constexpr int kQWarp = 18;                 // Q rows into shared memory (warp 19 idles)
+constexpr int kQWarp = 18;                 // warps 18-19: Q rows into shared memory
 constexpr int kEpiWarp0 = 20;              // warps 20-23: O of a finished segment
 constexpr int kEpiWarps = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
@@ -426,6 +428,7 @@ __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDe
   size_t at = 0;
   int rounded = 0;
   const int32_t* sp = nullptr;
+  uint32_t* ip = nullptr;
   const uint32_t* lut = nullptr;
   RowIndex index;
   uint32_t z = 0;
@@ -435,7 +438,9 @@ __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDe
     const HeadParamsDev hp = hp_s[a.per_head ? w.u : 0];
     index.set(hp, unbias(__ldcg(a.row_max + at)));
     lut = lut_s + 32 * hp.lut;
-    sp = a.scores + (static_cast<size_t>(w.b) * a.H + w.u) * a.ld_s + 4 * lane;
+    const size_t row = (static_cast<size_t>(w.b) * a.H + w.u) * a.ld_s + 4 * lane;
+    sp = a.scores + row;
+    ip = a.index + row / 4;
     rounded = (own_rows(a, w.b) + 31) & ~31;  // every score of a started 32-key block is set
     z = 0;
   };
@@ -447,7 +452,9 @@ __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDe
   for (int i = 0; i < n; ++i) {
     if (128 * w.blk + 4 * lane < rounded) {
       const int4 s = __ldcg(reinterpret_cast<const int4*>(sp + 128 * w.blk));
-      z += (lut[index(s.x)] + lut[index(s.y)]) + (lut[index(s.z)] + lut[index(s.w)]);
+      const uint32_t i0 = index(s.x), i1 = index(s.y), i2 = index(s.z), i3 = index(s.w);
+      z += (lut[i0] + lut[i1]) + (lut[i2] + lut[i3]);
+      ip[32 * w.blk] = prefill::pack4(i0, i1, i2, i3);
     }
     if (i + 1 < n && w.blk + 1 == w.nb) {
       leave();
@@ -488,34 +495,30 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, OwnRing& ring, const
   }
   size_t at = 0;
   int rows = 0, dh = 0;
-  const int32_t* sp = nullptr;
+  const uint32_t* ip = nullptr;
   const uint32_t* lut = nullptr;
-  RowIndex index;
-  unsigned long long R = 0;
+  uint32_t R = 0;  // < 2^25: Z is at least 2^15
   int32_t psum = 0;
   int32_t o[4][4];
-  int4 s0, s1;
+  uint32_t ix[2][2];  // indices of this block and the next
   auto enter = [&]() {
     dh = w.u % kHalves;
     const int u = w.u / kHalves, hk = u / groups, g0 = 8 * (u - hk * groups);
     rows = min(8, a.G - g0);
     at = static_cast<size_t>(hk) * a.R + w.b * a.G + g0;
     const int h = hk * a.G + g0 + min(n8, rows - 1);
-    sp = a.scores + (static_cast<size_t>(w.b) * a.H + h) * a.ld_s + 4 * t;
-    const HeadParamsDev hp = hp_s[a.per_head ? h : 0];
-    const size_t mine = at + min(n8, rows - 1);
-    index.set(hp, unbias(__ldcg(a.row_max + mine)));
-    R = exact_R(__ldcg(a.row_z + mine));
-    lut = lut_s + 32 * hp.lut;
+    ip = a.index + (static_cast<size_t>(w.b) * a.H + h) * (a.ld_s / 4) + t;
+    R = static_cast<uint32_t>(exact_R(__ldcg(a.row_z + at + min(n8, rows - 1))));
+    lut = lut_s + 32 * hp_s[a.per_head ? h : 0].lut;
     psum = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[c][i] = 0;
   };
-  auto load_scores = [&]() {
-    s0 = __ldcg(reinterpret_cast<const int4*>(sp + 32 * w.blk));
-    s1 = __ldcg(reinterpret_cast<const int4*>(sp + 32 * w.blk + 16));
+  auto load_index = [&](uint32_t (&x)[2], int blk) {
+    x[0] = __ldcg(ip + 8 * blk);
+    x[1] = __ldcg(ip + 8 * blk + 4);
   };
   auto leave = [&]() {
     if (a.v_u8 && dh == 0) {
@@ -535,28 +538,26 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, OwnRing& ring, const
       }
   };
   enter();
-  load_scores();
+  load_index(ix[0], w.blk);
   for (int i = 0; i < n; ++i) {
-    // P of this block (0 for rows the unit does not have)
-    uint32_t p[2];
-    {
-      const int32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          b[e] = static_cast<uint32_t>((lut[index(s[4 * g + e])] * R + (1ull << 31)) >> 32);
-        p[g] = n8 < rows ? prefill::pack4(b[0], b[1], b[2], b[3]) : 0u;
-        psum = static_cast<int32_t>(__dp4a(p[g], 0x01010101u, static_cast<uint32_t>(psum)));
-      }
-    }
     const bool last = i + 1 == n;
     const bool moves = !last && w.blk + 1 == w.nb;  // the next block is another unit's
-    if (!last && !moves) {
-      w.next(a, 32, units);
-      load_scores();
+    if (!last && !moves) load_index(ix[1], w.blk + 1);
+    // P of this block (0 for rows the unit does not have)
+    uint32_t p[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint32_t b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        b[e] = static_cast<uint32_t>(
+            (static_cast<unsigned long long>(lut[(ix[0][g] >> (8 * e)) & 255u]) * R + (1ull << 31)) >> 32);
+      p[g] = n8 < rows ? prefill::pack4(b[0], b[1], b[2], b[3]) : 0u;
+      psum = static_cast<int32_t>(__dp4a(p[g], 0x01010101u, static_cast<uint32_t>(psum)));
     }
+    if (!last && !moves) w.next(a, 32, units);
+    ix[0][0] = ix[1][0];
+    ix[0][1] = ix[1][1];
     const uint32_t tile = ring.wait(kRoleSoftmax);
     if (tile == 0) return false;
     uint2 v[8];
@@ -592,7 +593,7 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, OwnRing& ring, const
       leave();
       w.next(a, 32, units);
       enter();
-      load_scores();
+      load_index(ix[0], w.blk);
     }
   }
   leave();
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarQFull + i), 1);
+      mbar_init(bar(kBarQFull + i), 2);
       mbar_init(bar(kBarQEmpty + i), 1);
       mbar_init(bar(kBarSFull + i), 1);
       mbar_init(bar(kBarSEmpty + i), kTeamWarps);
@@ -1108,8 +1109,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     }
     mma_commit_elect(bar(kBarDrain));
     mbar_wait_warp(bar(kBarDrain), 0, kRoleMma);
-  } else if (warp == kQWarp) {
+  } else {
     // ============================== Q rows ==============================
+    // two warps, a half of the tile each, eight loads in flight per lane
     uint32_t nq = 0;
     bool ok = true;
     for (int phase = 0; phase < 3 && ok; ++phase)
@@ -1118,18 +1120,28 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         const uint32_t qb = nq & 1;
         if (!mbar_wait_warp(bar(kBarQEmpty + qb), ((nq >> 1) & 1) ^ 1, kRoleQ)) { ok = false; break; }
         constexpr int kPieces = D / 16;
-        for (int i = lane; i < kBM * kPieces; i += 32) {
-          const int rr = i / kPieces, c = i % kPieces;
-          const int row = sg.rt * kBM + rr;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row < args.R) {
-            const int b = row / args.G, g = row - b * args.G;
-            v = __ldg(reinterpret_cast<const uint4*>(
-                args.q + (static_cast<size_t>(b) * args.H + sg.hk * args.G + g) * D + 16 * c));
+        constexpr int kBatch = 8;
+        for (int i0 = (warp - kQWarp) * kBM / 2 * kPieces; i0 < (warp - kQWarp + 1) * kBM / 2 * kPieces; i0 += 32 * kBatch) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + 32 * k + lane;
+            const int row = sg.rt * kBM + i / kPieces;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (row < args.R) {
+              const int b = row / args.G, g = row - b * args.G;
+              v[k] = __ldg(reinterpret_cast<const uint4*>(
+                  args.q + (static_cast<size_t>(b) * args.H + sg.hk * args.G + g) * D + 16 * (i % kPieces)));
+            }
           }
-          // the TMA's swizzle: 16-byte piece c of row rr
-          const int sw = D == 128 ? (c ^ (rr & 7)) : (c ^ ((rr >> 1) & 3));
-          *reinterpret_cast<uint4*>(smem + C::kOffQ + qb * C::kQBytes + rr * D + 16 * sw) = v;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + 32 * k + lane;
+            const int rr = i / kPieces, c = i % kPieces;
+            // the TMA's swizzle: 16-byte piece c of row rr
+            const int piece = D == 128 ? (c ^ (rr & 7)) : (c ^ ((rr >> 1) & 3));
+            *reinterpret_cast<uint4*>(smem + C::kOffQ + qb * C::kQBytes + rr * D + 16 * piece) = v[k];
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
