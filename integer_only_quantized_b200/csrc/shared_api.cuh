@@ -47,7 +47,7 @@ SharedLayout shared_layout(long long BH, int Lmax, int d) {
   L.off_acc = (L.off_z + 8 * rows + 15) & ~size_t(15);
   L.off_z = L.off_acc - 8 * rows;
   L.off_p = L.off_z + 4 * rows;
-  L.ld_s = (Lmax + 31) & ~31;  // whole 32-key blocks
+  L.ld_s = (Lmax + 31) & ~31;  // whole blocks
   L.off_s = round256(L.off_acc + 4 * rows * d);
   L.off_i = L.off_s + round256(4 * rows * static_cast<size_t>(L.ld_s));
   L.total = L.off_i + round256(rows * static_cast<size_t>(L.ld_s));
@@ -88,17 +88,16 @@ int shared_launch(const SharedArgs& a, int grid, const SharedLayout& L, cudaStre
 }
 
 // [planes, rows of capacity, d] bytes with the first `rows` rows of a plane
-// visible (rows past them read as 0), box {box_x, box_rows, 1}, swizzle = box_x bytes.
-bool encode_rows(CUtensorMap* m, const void* base, int d, int rows, int capacity, long long planes, int box_x,
-                 int box_rows) {
+// visible (rows past them read as 0), box {d, box_rows, 1}, swizzle = d bytes.
+bool encode_rows(CUtensorMap* m, const void* base, int d, int rows, int capacity, long long planes, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(capacity) * d};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_rows), 1u};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows), 1u};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, box_x == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -164,18 +163,23 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   a.k_u8 = scales->z_k ? 1 : 0;
   a.v_u8 = scales->z_v ? 1 : 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const long long tiles = static_cast<long long>(Hkv) * a.row_tiles * a.key_tiles;
-  if (tiles > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
-  a.tiles = static_cast<int32_t>(tiles);
-  if (Lp > 0 && (!encode_rows(&a.tm_k, k_prefix, d, Lp, Lp_max, Hkv, d, intattn::shared::kBN) ||
-                 !encode_rows(&a.tm_v, v_prefix, d, Lp, Lp_max, Hkv, d, intattn::shared::kBN)))
-    return INTATTN_ERR_CUDA;
-  const long long planes = static_cast<long long>(B) * Hkv;
-  if (Lmax > 0 && (!encode_rows(&a.tm_kc, k_cache, d, Lmax, Lmax, planes, d, 2048 / d) ||
-                   !encode_rows(&a.tm_vc, v_cache, d, Lmax, Lmax, planes, 64, 32)))
-    return INTATTN_ERR_CUDA;
   int sms = 0;
   if (sm_count(&sms) != INTATTN_OK) return INTATTN_ERR_CUDA;
+  // few queries fold F key tiles into a tile, as long as every SM still gets one
+  a.fold = 1;
+  for (int f = 2; f <= 4; f *= 2)
+    if (a.R <= intattn::shared::kBM / f && static_cast<long long>(Hkv) * ((a.key_tiles + f - 1) / f) >= sms) a.fold = f;
+  a.seg_tiles = (a.key_tiles + a.fold - 1) / a.fold;
+  const long long tiles = static_cast<long long>(Hkv) * a.row_tiles * a.seg_tiles;
+  if (tiles > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
+  a.tiles = static_cast<int32_t>(tiles);
+  if (Lp > 0 && (!encode_rows(&a.tm_k, k_prefix, d, Lp, Lp_max, Hkv, intattn::shared::kBN) ||
+                 !encode_rows(&a.tm_v, v_prefix, d, Lp, Lp_max, Hkv, intattn::shared::kBN)))
+    return INTATTN_ERR_CUDA;
+  const long long planes = static_cast<long long>(B) * Hkv;
+  if (Lmax > 0 && (!encode_rows(&a.tm_kc, k_cache, d, Lmax, Lmax, planes, 2048 / d) ||
+                   !encode_rows(&a.tm_vc, v_cache, d, Lmax, Lmax, planes, 2048 / d)))
+    return INTATTN_ERR_CUDA;
   // as many CTAs as there are prefix tiles or 128-key pieces of own rows
   const long long own = static_cast<long long>(B) * Hkv * ((Lmax + 127) / 128);
   const int grid = static_cast<int>(std::min<long long>(sms, std::max<long long>(std::max(tiles, own), 1)));
