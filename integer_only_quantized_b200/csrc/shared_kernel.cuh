@@ -36,7 +36,7 @@
 // Own rows.  They are read by one sequence only: an HBM stream with up to
 // eight query rows per K / V row.  Each of the own warps takes an equal
 // consecutive share of all blocks of own rows (2 KB each) and streams it through
-// a ring of its own TMA tiles: 48 KB in flight per SM, no registers held by loads, no
+// a ring of its own TMA tiles: 80 KB in flight per SM, no registers held by loads, no
 // barrier shared by warps.  The products are m16n8k32 and m16n8k16 integer MMAs, keys or
 // channels on the 16 side and the grouped heads on the 8 side; the contraction
 // order is free, so a thread's consecutive bytes serve as its fragments.  Scores
@@ -102,7 +102,7 @@ constexpr int kMmaWarp = 17;
 constexpr int kQWarp = 18;                 // warps 18-19: Q rows into shared memory
 constexpr int kOwnWarp0 = 20;              // warps 20-27: own rows
 constexpr int kOwnWarps = 8;
-constexpr int kOwnSlots = 3;               // 2 KB tiles per own warp
+constexpr int kOwnSlots = 5;               // 2 KB tiles per own warp
 constexpr int kThreads = 32 * (kOwnWarp0 + kOwnWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;              // two S buffers
@@ -130,7 +130,7 @@ enum Bar : int {
 
 template <int D>
 struct Cfg {
-  static constexpr int kStages = (D == 64) ? 8 : 5;
+  static constexpr int kStages = (D == 64) ? 8 : 4;
   static constexpr uint32_t kTileBytes = kBN * D;
   static constexpr uint32_t kSwizzle = (D == 128) ? 2u : 4u;  // 128B / 64B swizzle
   static constexpr uint32_t kSBO = 8 * D;
@@ -151,7 +151,8 @@ struct Cfg {
   static constexpr uint32_t kUsed = kOffMisc + 16;
   static_assert(kOffKV % 1024 == 0 && kOffOwn % 1024 == 0, "swizzled tiles");
   // one CTA per SM: every CTA takes all 512 TMEM columns
-  static constexpr uint32_t kSmemBytes = (kUsed + 1024 > 120 * 1024) ? kUsed + 1024 : 120 * 1024;
+  // (dynamic shared memory starts on 128 bytes: at most 896 go to the alignment)
+  static constexpr uint32_t kSmemBytes = (kUsed + 896 > 120 * 1024) ? kUsed + 896 : 120 * 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -218,38 +219,67 @@ __device__ __forceinline__ void mma16816(int32_t (&c)[4], uint32_t a0, uint32_t 
 // The blocks of `keys` own rows of every sequence and unit (K / V head, group
 // of eight query heads), in the order (b, unit, block), and a warp's
 // place among them.  Warp-collective.
+constexpr int kUnitCost = 1;  // blocks' worth of work in changing the unit, for equal shares
 struct Walk {
   int b, u, blk, nb;  // nb: blocks of sequence b
   // the share of warp `w` of `warps`: its first block (where there is one), and their number
   __device__ __forceinline__ int share(const SharedArgs& a, int keys, int units, int w, int warps) {
     const int lane = threadIdx.x & 31;
+    auto blocks = [&](int i) { return i < a.B ? (own_rows(a, i) + keys - 1) / keys : 0; };
+    auto cost = [&](int n) { return n > 0 ? n + kUnitCost : 0; };
     int total = 0;
-    for (int i = lane; i < a.B; i += 32) total += (own_rows(a, i) + keys - 1) / keys;
+    for (int i = lane; i < a.B; i += 32) total += cost(blocks(i));
     total = __reduce_add_sync(0xffffffffu, total) * units;
     const int each = total / warps, more = total - each * warps;
-    int p = each * w + min(w, more);
-    const int n = each + (w < more ? 1 : 0);
+    int p[2];  // the share's ends, in units of cost from the current sequences on
+    p[0] = each * w + min(w, more);
+    p[1] = p[0] + each + (w < more ? 1 : 0);
+    int at[2] = {0, 0};  // blocks before them
+    bool found[2] = {false, false};
     b = u = blk = nb = 0;
-    if (n == 0) return 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int mine = b0 + lane < a.B ? (own_rows(a, b0 + lane) + keys - 1) / keys : 0;
-      int incl = mine * units;
+    for (int b0 = 0; b0 < a.B && !found[1]; b0 += 32) {
+      const int mine = blocks(b0 + lane);
+      int c = cost(mine), n = mine;  // sums up to and with this lane's sequence
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+        const int c_up = __shfl_up_sync(0xffffffffu, c, o), n_up = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) {
+          c += c_up;
+          n += n_up;
+        }
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, incl > p);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        nb = __shfl_sync(0xffffffffu, mine, l);
-        p -= __shfl_sync(0xffffffffu, incl, l) - nb * units;
-        b = b0 + l;
-        u = p / nb;
-        blk = p - u * nb;
-        break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (found[e]) continue;
+        const uint32_t past = __ballot_sync(0xffffffffu, c * units > p[e]);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          const int k = __shfl_sync(0xffffffffu, mine, l);
+          const int q = p[e] - (__shfl_sync(0xffffffffu, c, l) - cost(k)) * units;  // within sequence b0 + l
+          int v = q / cost(k), o = q - v * cost(k);
+          if (o >= k) {  // between two units: the next one's first block
+            ++v;
+            o = 0;
+          }
+          at[e] += (__shfl_sync(0xffffffffu, n, l) - k) * units + v * k + o;
+          found[e] = true;
+          if (e == 0) {
+            b = b0 + l;
+            u = v;
+            blk = o;
+            nb = k;
+          }
+        } else {
+          at[e] += __shfl_sync(0xffffffffu, n, 31) * units;
+          p[e] -= __shfl_sync(0xffffffffu, c, 31) * units;
+        }
       }
-      p -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int n = at[1] - at[0];
+    if (n > 0 && u == units) {  // the first block is the next sequence's
+      u = units - 1;
+      blk = nb - 1;
+      next(a, keys, units);
     }
     return n;
   }
@@ -693,6 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
+  if (smem + C::kUsed > smem_raw + C::kSmemBytes) {  // the alignment took more than its share: nothing runs
+    if (tid == 0) atomicOr(&g_device_error, kErrTimeout);
+    return;
+  }
   const int F = args.fold;
   const int RF = kBM / F;       // lanes per fold
   const int psets = kPBufs / F; // sets of F P buffers
@@ -700,9 +734,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   const int t0 = static_cast<int>(static_cast<long long>(args.tiles) * blockIdx.x / gridDim.x);
   const int t1 = static_cast<int>(static_cast<long long>(args.tiles) * (blockIdx.x + 1) / gridDim.x);
 
+  // The queries of at most two segments stay in the two Q buffers through all
+  // phases, loaded by the softmax warps; of more, two warps load them again in every phase.
+  const bool q_stays = t0 < t1 && (t1 - 1) / args.seg_tiles - t0 / args.seg_tiles < 2;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarQFull + i), 2);
+      mbar_init(bar(kBarQFull + i), q_stays ? kSoftWarps : 2);
       mbar_init(bar(kBarQEmpty + i), 1);
       mbar_init(bar(kBarSFull + i), 1);
       mbar_init(bar(kBarSEmpty + i), kTeamWarps);
@@ -735,15 +772,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   // Grid-wide barrier k, reached by all softmax and own warps: whether every
   // warp's work so far was done and every CTA arrived in time.
   auto grid_sync = [&](int k, bool ok) {
-    __threadfence();
     const bool v = bar_red_and(kNbBoth, 32 * (kSoftWarps + kOwnWarps), ok);
     if (tid == 0) {
       uint32_t good = 0;
       if (v) {
-        __threadfence();
-        atomicAdd(args.ctr + k, 1u);
+        // release and acquire at gpu scope by one thread cover the CTA's
+        // other threads, which the named barriers order with it
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(args.ctr + k) : "memory");
         good = quant::wait_count(args.ctr + k, gridDim.x) ? 1u : 0u;
-        __threadfence();
       }
       *verdict = good;
     }
@@ -751,6 +787,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     return *verdict != 0u;
   };
   constexpr int kFinishers = 32 * (kSoftWarps + kOwnWarps);
+  constexpr int kPieces = D / 16;  // of a row
+  // piece i of the query rows of a segment (16-byte pieces, row by row)
+  auto q_piece = [&](const Segment& sg, int i) {
+    const int row = sg.rt * kBM + i / kPieces;
+    if (i >= RF * kPieces || row >= args.R) return make_uint4(0, 0, 0, 0);
+    const int b = row / args.G, g = row - b * args.G;
+    return __ldg(reinterpret_cast<const uint4*>(args.q + (static_cast<size_t>(b) * args.H + sg.hk * args.G + g) * D +
+                                                16 * (i % kPieces)));
+  };
+  auto q_store = [&](uint32_t qb, int i, uint4 v) {
+    if (i >= RF * kPieces) return;
+    const int row = kBM - RF + kBM * static_cast<int>(qb) + i / kPieces, c = i % kPieces;
+    const int piece = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));  // the TMA's swizzle
+    *reinterpret_cast<uint4*>(smem + C::kOffQ + row * D + 16 * piece) = v;
+  };
+  auto q_zero = [&](int worker, int workers) {  // the padding rows: zero for good
+    for (int i = worker; i < C::kQRows * kPieces; i += workers)
+      *reinterpret_cast<uint4*>(smem + C::kOffQ + 16 * i) = make_uint4(0, 0, 0, 0);
+  };
   // Registers: 896 threads are launched with 72 each; the softmax warps give 8
   // each (4096 in all), which is what the own warps take (16 each).
   if (warp < kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -787,6 +842,30 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(b);
     };
+    if (q_stays) {
+      const Segment sg = segment_at(args, t0, t1);
+      const bool two = t0 + sg.n < t1;
+      const Segment sh = two ? segment_at(args, t0 + sg.n, t1) : sg;
+      constexpr int kPer = kBM * kPieces / (32 * kSoftWarps);  // 1 or 2 pieces per thread and segment
+      uint4 v[2][kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        v[0][k] = q_piece(sg, tid + 32 * kSoftWarps * k);
+        v[1][k] = q_piece(sh, tid + 32 * kSoftWarps * k);
+      }
+      if (F > 1) {
+        q_zero(tid, 32 * kSoftWarps);
+        soft_sync(true);
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        q_store(0, tid + 32 * kSoftWarps * k, v[0][k]);
+        if (two) q_store(1, tid + 32 * kSoftWarps * k, v[1][k]);
+      }
+      fence_proxy_async_smem();
+      arrive_warp(bar(kBarQFull));
+      if (two) arrive_warp(bar(kBarQFull + 1));
+    }
     // The scores of tile `idx`, 32 columns at a time; columns from nv on are
     // `low`.  One copy of the body in a rolled loop: the phases' code has to
     // stay small (instruction fetches were a third of the stalls with both
@@ -1068,41 +1147,74 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     constexpr uint32_t kSlotDesc = C::kTileBytes >> 4;
     bool ok = true;
     uint32_t slot = 0, kv_par = 0, sc = 0, pc = 0, nq = 0, no = 0;
-    auto next_slot = [&]() {
-      if (++slot == static_cast<uint32_t>(C::kStages)) {
-        slot = 0;
+    // Waits, all at once: lane 0 for the tile's own barrier, lanes 1 .. nf for
+    // the K or V tiles in the next nf ring slots, lane 31 for one more barrier.
+    auto wait_tiles = [&](int nf, uint32_t own_bar, uint32_t own_par, uint32_t more_bar, uint32_t more_par) {
+      uint32_t b = own_bar, par = own_par;
+      bool mine = lane <= nf;
+      if (lane > 0) {
+        const uint32_t s = slot + lane - 1;
+        const bool wraps = s >= static_cast<uint32_t>(C::kStages);
+        b = bar_kv_full(wraps ? s - C::kStages : s);
+        par = kv_par ^ (wraps ? 1u : 0u);
+      }
+      if (lane == 31 && more_bar != 0) {
+        b = more_bar;
+        par = more_par;
+        mine = true;
+      }
+      bool done = !mine || mbar_try_wait(b, par);
+      if (__all_sync(0xffffffffu, done)) return true;
+      const unsigned long long start = globaltimer_ns();
+      while (true) {
+        if (!done) done = mbar_try_wait(b, par);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - start > kWaitTimeoutNs)) {
+          if (lane == 0) atomicOr(&g_device_error, kErrTimeout | (kRoleMma << 8));
+          return false;
+        }
+      }
+    };
+    auto step = [](uint32_t s) { return s + 1 == static_cast<uint32_t>(C::kStages) ? 0u : s + 1; };
+    auto advance = [&](int nf) {
+      slot += nf;
+      if (slot >= static_cast<uint32_t>(C::kStages)) {
+        slot -= C::kStages;
         kv_par ^= 1;
       }
     };
+    static_assert(C::kStages >= 4, "the key tiles of a tile fit the ring");
     for (int phase = 0; phase < 3 && ok; ++phase) {
+      if (q_stays) nq = 0;
       for (int t = t0; t < t1 && ok; ++nq) {
         const Segment sg = segment_at(args, t, t1);
         const uint32_t qb = nq & 1;
-        if (!mbar_wait_warp(bar(kBarQFull + qb), (nq >> 1) & 1, kRoleMma)) { ok = false; break; }
+        if (!mbar_wait_warp(bar(kBarQFull + qb), q_stays ? 0u : (nq >> 1) & 1, kRoleMma)) { ok = false; break; }
+        const uint64_t q_desc = q_desc0 + ((static_cast<uint32_t>(kBM - RF + kBM * qb) * D) >> 4);
         // S of tile j: the queries in the lanes of fold x against key tile x
         auto issue_qk = [&](int j) {
           if (!ok) return;
           const uint32_t buf = sc & 1;
           const int nf = folds_at(args, j);
-          for (int x = 0; x < nf; ++x) {
-            if (!(x == 0 ? mbar_wait2_warp(bar(kBarSEmpty + buf), ((sc >> 1) & 1) ^ 1, bar_kv_full(slot), kv_par, kRoleMma)
-                         : mbar_wait_warp(bar_kv_full(slot), kv_par, kRoleMma))) {
-              ok = false;
-              return;
-            }
-            tc_fence_after();
-            const uint64_t k_desc = kv_desc0 + slot * kSlotDesc;
-            const uint64_t q_desc = q_desc0 + ((static_cast<uint32_t>(kBM - RF + kBM * qb - x * RF) * D) >> 4);
-            if (elect_one()) {
+          if (!wait_tiles(nf, bar(kBarSEmpty + buf), ((sc >> 1) & 1) ^ 1, 0u, 0u)) {
+            ok = false;
+            return;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            uint32_t sl = slot;
+            for (int x = 0; x < nf; ++x, sl = step(sl)) {
+              const uint64_t k_desc = kv_desc0 + sl * kSlotDesc;
+              const uint64_t a_desc = q_desc - ((static_cast<uint32_t>(x * RF) * D) >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
-                mma_i8_ss(tmem + kColS + buf * kBN, q_desc + 2 * kk, k_desc + 2 * kk, idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
-              mma_commit(bar_kv_empty(slot));
-              if (x == nf - 1) mma_commit(bar(kBarSFull + buf));
+                mma_i8_ss(tmem + kColS + buf * kBN, a_desc + 2 * kk, k_desc + 2 * kk, idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(bar_kv_empty(sl));
             }
-            __syncwarp();
-            next_slot();
+            mma_commit(bar(kBarSFull + buf));
           }
+          __syncwarp();
+          advance(nf);
           ++sc;
         };
         if (phase < 2) {
@@ -1113,35 +1225,35 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           for (int j = 0; ok && j < sg.n; ++j, ++pc) {
             if (j + 2 < sg.n) issue_qk(sg.j0 + j + 2);
             if (!ok) break;
-            if (j == 0 && !mbar_wait_warp(bar(kBarOEmpty), (no & 1) ^ 1, kRoleMma)) { ok = false; break; }
             const uint32_t set = pc & (psets - 1);
             const int nf = folds_at(args, sg.j0 + j);
-            for (int x = 0; x < nf; ++x) {
-              if (!(x == 0 ? mbar_wait2_warp(bar(kBarPFull + set), (pc / psets) & 1, bar_kv_full(slot), kv_par, kRoleMma)
-                           : mbar_wait_warp(bar_kv_full(slot), kv_par, kRoleMma))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint64_t v_desc = kv_desc0 + slot * kSlotDesc;
-              if (elect_one()) {
+            // the first P.V of a segment: O of the previous one has been read
+            if (!wait_tiles(nf, bar(kBarPFull + set), (pc / psets) & 1, j == 0 ? bar(kBarOEmpty) : 0u, (no & 1) ^ 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              uint32_t sl = slot;
+              for (int x = 0; x < nf; ++x, sl = step(sl)) {
+                const uint64_t v_desc = kv_desc0 + sl * kSlotDesc;
 #pragma unroll
                 for (int kk = 0; kk < kBN / 32; ++kk)
                   mma_i8_ts(tmem + kColO, tmem + kColP + (set * F + x) * 32 + kk * 8, v_desc + ((32u * D * kk) >> 4),
                             idesc_pv, (j > 0 || x > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(bar_kv_empty(slot));
-                if (x == nf - 1) mma_commit(bar(kBarPEmpty + set));
+                mma_commit(bar_kv_empty(sl));
               }
-              __syncwarp();
-              next_slot();
+              mma_commit(bar(kBarPEmpty + set));
             }
+            __syncwarp();
+            advance(nf);
           }
           if (!ok) break;
           mma_commit_elect(bar(kBarOFull));
           ++no;
         }
         if (!ok) break;
-        mma_commit_elect(bar(kBarQEmpty + qb));
+        if (!q_stays) mma_commit_elect(bar(kBarQEmpty + qb));
         t += sg.n;
       }
     }
@@ -1149,50 +1261,34 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     mbar_wait_warp(bar(kBarDrain), 0, kRoleMma);
   } else {
     // ============================== Q rows ==============================
-    // two warps, a half of the rows each, eight loads in flight per lane
-    constexpr int kPieces = D / 16;
-    constexpr int kBatch = 8;
-    const int qw = warp - kQWarp;
-    if (F > 1)  // the padding rows: zero for good
-      for (int i = qw * 32 + lane; i < C::kQRows * kPieces; i += 64)
-        *reinterpret_cast<uint4*>(smem + C::kOffQ + 16 * i) = make_uint4(0, 0, 0, 0);
-    uint32_t nq = 0;
-    bool ok = true;
-    if (F > 1) asm volatile("bar.sync 3, 64;" ::: "memory");  // both warps' zeros before the first rows
-    for (int phase = 0; phase < 3 && ok; ++phase)
-      for (int t = t0; t < t1; ++nq) {
-        const Segment sg = segment_at(args, t, t1);
-        const uint32_t qb = nq & 1;
-        if (!mbar_wait_warp(bar(kBarQEmpty + qb), ((nq >> 1) & 1) ^ 1, kRoleQ)) { ok = false; break; }
-        const int row0 = kBM - RF + kBM * static_cast<int>(qb);  // of the buffer
-        const int end = (qw + 1) * (RF / 2) * kPieces;
-        for (int i0 = qw * (RF / 2) * kPieces; i0 < end; i0 += 32 * kBatch) {
-          uint4 v[kBatch];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int i = i0 + 32 * k + lane;
-            const int row = sg.rt * kBM + i / kPieces;
-            v[k] = make_uint4(0, 0, 0, 0);
-            if (i < end && row < args.R) {
-              const int b = row / args.G, g = row - b * args.G;
-              v[k] = __ldg(reinterpret_cast<const uint4*>(
-                  args.q + (static_cast<size_t>(b) * args.H + sg.hk * args.G + g) * D + 16 * (i % kPieces)));
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int i = i0 + 32 * k + lane;
-            const int row = row0 + i / kPieces, c = i % kPieces;
-            // the TMA's swizzle: 16-byte piece c of a row
-            const int piece = D == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
-            if (i < end) *reinterpret_cast<uint4*>(smem + C::kOffQ + row * D + 16 * piece) = v[k];
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarQFull + qb));
-        t += sg.n;
+    // more than two segments: a half of the rows each, eight loads in flight per lane
+    if (!q_stays && t0 < t1) {
+      constexpr int kBatch = 8;
+      const int qw = warp - kQWarp;
+      if (F > 1) {
+        q_zero(qw * 32 + lane, 64);
+        asm volatile("bar.sync 3, 64;" ::: "memory");  // both warps' zeros before the first rows
       }
+      uint32_t nq = 0;
+      bool ok = true;
+      for (int phase = 0; phase < 3 && ok; ++phase)
+        for (int t = t0; t < t1; ++nq) {
+          const Segment sg = segment_at(args, t, t1);
+          const uint32_t qb = nq & 1;
+          if (!mbar_wait_warp(bar(kBarQEmpty + qb), ((nq >> 1) & 1) ^ 1, kRoleQ)) { ok = false; break; }
+          for (int i0 = 32 * qw; i0 < RF * kPieces; i0 += 64 * kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) v[k] = q_piece(sg, i0 + 64 * k + lane);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) q_store(qb, i0 + 64 * k + lane, v[k]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarQFull + qb));
+          t += sg.n;
+        }
+    }
   }
 
   tc_fence_before();
