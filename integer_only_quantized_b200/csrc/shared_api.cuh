@@ -47,21 +47,21 @@ SharedLayout shared_layout(long long BH, int Lmax, int d) {
   L.off_acc = (L.off_z + 8 * rows + 15) & ~size_t(15);
   L.off_z = L.off_acc - 8 * rows;
   L.off_p = L.off_z + 4 * rows;
-  L.ld_s = (Lmax + 31) & ~31;  // whole blocks
+  L.ld_s = (Lmax + 63) & ~63;  // whole blocks
   L.off_s = round256(L.off_acc + 4 * rows * d);
   L.off_i = L.off_s + round256(4 * rows * static_cast<size_t>(L.ld_s));
   L.total = L.off_i + round256(rows * static_cast<size_t>(L.ld_s));
   return L;
 }
 
-template <int D>
+template <int D, bool ZP>
 int shared_launch(const SharedArgs& a, int grid, const SharedLayout& L, cudaStream_t st) {
   using C = intattn::shared::Cfg<D>;
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return INTATTN_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(intattn::shared::shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(intattn::shared::shared_kernel<D, ZP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(C::kSmemBytes)) != cudaSuccess)
       return note_launch(cudaGetLastError());
     attr_set[dev] = true;
@@ -84,7 +84,7 @@ int shared_launch(const SharedArgs& a, int grid, const SharedLayout& L, cudaStre
   cfg.stream = st;
   cfg.attrs = attrs;
   cfg.numAttrs = 2;
-  return note_launch(cudaLaunchKernelEx(&cfg, intattn::shared::shared_kernel<D>, a));
+  return note_launch(cudaLaunchKernelEx(&cfg, intattn::shared::shared_kernel<D, ZP>, a));
 }
 
 // [planes, rows of capacity, d] bytes with the first `rows` rows of a plane
@@ -177,13 +177,14 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
                  !encode_rows(&a.tm_v, v_prefix, d, Lp, Lp_max, Hkv, intattn::shared::kBN)))
     return INTATTN_ERR_CUDA;
   const long long planes = static_cast<long long>(B) * Hkv;
-  if (Lmax > 0 && (!encode_rows(&a.tm_kc, k_cache, d, Lmax, Lmax, planes, 2048 / d) ||
-                   !encode_rows(&a.tm_vc, v_cache, d, Lmax, Lmax, planes, 2048 / d)))
+  if (Lmax > 0 && (!encode_rows(&a.tm_kc, k_cache, d, Lmax, Lmax, planes, intattn::shared::kOwnBytes / d) ||
+                   !encode_rows(&a.tm_vc, v_cache, d, Lmax, Lmax, planes, intattn::shared::kOwnBytes / d)))
     return INTATTN_ERR_CUDA;
   // as many CTAs as there are prefix tiles or 128-key pieces of own rows
   const long long own = static_cast<long long>(B) * Hkv * ((Lmax + 127) / 128);
   const int grid = static_cast<int>(std::min<long long>(sms, std::max<long long>(std::max(tiles, own), 1)));
-  return d == 64 ? shared_launch<64>(a, grid, L, st) : shared_launch<128>(a, grid, L, st);
+  if (a.k_u8 || a.v_u8) return d == 64 ? shared_launch<64, true>(a, grid, L, st) : shared_launch<128, true>(a, grid, L, st);
+  return d == 64 ? shared_launch<64, false>(a, grid, L, st) : shared_launch<128, false>(a, grid, L, st);
 }
 
 }  // extern "C"

@@ -35,8 +35,8 @@
 //
 // Own rows.  They are read by one sequence only: an HBM stream with up to
 // eight query rows per K / V row.  Each of the own warps takes an equal
-// consecutive share of all blocks of own rows (2 KB each) and streams it through
-// a ring of its own TMA tiles: 80 KB in flight per SM, no registers held by loads, no
+// consecutive share of all blocks of own rows (4 KB each) and streams it through
+// a ring of its own TMA tiles: 64 KB in flight per SM, no registers held by loads, no
 // barrier shared by warps.  The products are m16n8k32 and m16n8k16 integer MMAs, keys or
 // channels on the 16 side and the grouped heads on the 8 side; the contraction
 // order is free, so a thread's consecutive bytes serve as its fragments.  Scores
@@ -61,7 +61,7 @@ namespace intattn {
 
 struct SharedArgs {
   CUtensorMap tm_k, tm_v;     // prefix [Hkv, Lp, d], box {d, 128, 1}
-  CUtensorMap tm_kc, tm_vc;   // own rows [B Hkv, Lmax, d], box {d, 2048 / d, 1}
+  CUtensorMap tm_kc, tm_vc;   // own rows [B Hkv, Lmax, d], box {d, 4096 / d, 1}
   const int8_t* q;            // [B, H, d]
   const int32_t* lengths;     // [B], or null: Lmax
   void* out;                  // [B, H, d] int8 codes, or fp16 / bf16 values
@@ -102,7 +102,8 @@ constexpr int kMmaWarp = 17;
 constexpr int kQWarp = 18;                 // warps 18-19: Q rows into shared memory
 constexpr int kOwnWarp0 = 20;              // warps 20-27: own rows
 constexpr int kOwnWarps = 8;
-constexpr int kOwnSlots = 5;               // 2 KB tiles per own warp
+constexpr int kOwnBytes = 4096;            // bytes of an own-row block
+constexpr int kOwnSlots = 2;               // blocks in an own warp's ring
 constexpr int kThreads = 32 * (kOwnWarp0 + kOwnWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;              // two S buffers
@@ -130,7 +131,7 @@ enum Bar : int {
 
 template <int D>
 struct Cfg {
-  static constexpr int kStages = (D == 64) ? 8 : 4;
+  static constexpr int kStages = (D == 64) ? 8 : 5;
   static constexpr uint32_t kTileBytes = kBN * D;
   static constexpr uint32_t kSwizzle = (D == 128) ? 2u : 4u;  // 128B / 64B swizzle
   static constexpr uint32_t kSBO = 8 * D;
@@ -143,7 +144,7 @@ struct Cfg {
   // per-row tables [33][kBM] u32, row k for index code k (see idx_bits2; 1 .. 32): in
   // phase B the first holds LUT, in phase C table b holds P << 8b
   static constexpr uint32_t kTabBytes = 33 * kBM * 4;
-  static constexpr uint32_t kOffTab = kOffOwn + kOwnWarps * kOwnSlots * 2048;
+  static constexpr uint32_t kOffTab = kOffOwn + kOwnWarps * kOwnSlots * kOwnBytes;
   static constexpr uint32_t kOffLut = kOffTab + 2 * kTabBytes;
   static constexpr uint32_t kOffHp = kOffLut + INTATTN_MAX_CLIPS * 32 * 4;
   static constexpr uint32_t kOffBars = kOffHp + INTATTN_MAX_HEADS * sizeof(HeadParamsDev);
@@ -180,22 +181,24 @@ __device__ __forceinline__ void red_add4(float* p, float a, float b, float c, fl
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
-// D[16 x 8] += A[16 x 32] B[32 x 8], bytes, row x column fragments.
-template <bool kASigned, bool kBSigned>
-__device__ __forceinline__ void mma16832(int32_t (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+// D[16 x 8] += A[16 x 32] B[32 x 8], row x column fragments: A s8 or u8 (K), B s8 (queries).
+__device__ __forceinline__ void mma16832(int32_t (&c)[4], bool a_u8, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  if constexpr (kASigned && kBSigned)
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else if constexpr (kBSigned)
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else if constexpr (kASigned)
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  if (a_u8)
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D[16 x 8] += A[16 x 16] B[16 x 8]: A s8 or u8 (V), B u8 (P).
+__device__ __forceinline__ void mma16816(int32_t (&c)[4], bool a_u8, uint32_t a0, uint32_t a1, uint32_t b0) {
+  if (a_u8)
+    asm("mma.sync.aligned.m16n8k16.row.col.s32.u8.u8.s32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
 }
 
 // Own rows of a sequence; 0 for a length out of range (its output is skipped).
@@ -205,26 +208,16 @@ __device__ __forceinline__ int own_rows(const SharedArgs& a, int b) {
   return n < 0 || n > a.Lmax ? 0 : n;
 }
 
-// D[16 x 8] += A[16 x 16] B[16 x 8]: A s8 or u8, B u8.
-template <bool kASigned>
-__device__ __forceinline__ void mma16816(int32_t (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  if constexpr (kASigned)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.s32.u8.u8.s32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
-}
-
 // The blocks of `keys` own rows of every sequence and unit (K / V head, group
 // of eight query heads), in the order (b, unit, block), and a warp's
 // place among them.  Warp-collective.
 constexpr int kUnitCost = 1;  // blocks' worth of work in changing the unit, for equal shares
 struct Walk {
-  int b, u, blk, nb;  // nb: blocks of sequence b
+  int b, hk, g, blk, nb;  // sequence, K / V head, group of eight query heads; nb: blocks of the sequence
   // the share of warp `w` of `warps`: its first block (where there is one), and their number
-  __device__ __forceinline__ int share(const SharedArgs& a, int keys, int units, int w, int warps) {
+  __device__ __forceinline__ int share(const SharedArgs& a, int keys, int w, int warps) {
     const int lane = threadIdx.x & 31;
+    const int groups = (a.G + 7) / 8, units = a.Hkv * groups;
     auto blocks = [&](int i) { return i < a.B ? (own_rows(a, i) + keys - 1) / keys : 0; };
     auto cost = [&](int n) { return n > 0 ? n + kUnitCost : 0; };
     int total = 0;
@@ -236,7 +229,8 @@ struct Walk {
     p[1] = p[0] + each + (w < more ? 1 : 0);
     int at[2] = {0, 0};  // blocks before them
     bool found[2] = {false, false};
-    b = u = blk = nb = 0;
+    b = hk = g = blk = nb = 0;
+    int u = 0;
     for (int b0 = 0; b0 < a.B && !found[1]; b0 += 32) {
       const int mine = blocks(b0 + lane);
       int c = cost(mine), n = mine;  // sums up to and with this lane's sequence
@@ -276,24 +270,28 @@ struct Walk {
       }
     }
     const int n = at[1] - at[0];
-    if (n > 0 && u == units) {  // the first block is the next sequence's
-      u = units - 1;
+    const bool over = u == units;  // the first block is the next sequence's
+    if (over) {
+      --u;
       blk = nb - 1;
-      next(a, keys, units);
     }
+    hk = u / groups;
+    g = u - hk * groups;
+    if (n > 0 && over) next(a, keys);
     return n;
   }
   // to the next block (there is one)
-  __device__ __forceinline__ void next(const SharedArgs& a, int keys, int units) {
+  __device__ __forceinline__ void next(const SharedArgs& a, int keys) {
     if (++blk < nb) return;
     blk = 0;
-    if (++u == units) {
-      u = 0;
-      do {
-        ++b;
-        nb = (own_rows(a, b) + keys - 1) / keys;
-      } while (nb == 0);
-    }
+    if (8 * ++g < a.G) return;
+    g = 0;
+    if (++hk < a.Hkv) return;
+    hk = 0;
+    do {
+      ++b;
+      nb = (own_rows(a, b) + keys - 1) / keys;
+    } while (nb == 0);
   }
 };
 
@@ -301,29 +299,25 @@ struct Walk {
 struct Unit {
   int head, rows, len;  // first query head; 1 .. 8 of them; own rows of the sequence
   int at, row;          // first row in the row arrays; in [B, H]
-  __device__ __forceinline__ void set(const SharedArgs& a, const Walk& w, int groups) {
-    const int hk = w.u / groups, g0 = 8 * (w.u - hk * groups);
+  __device__ __forceinline__ void set(const SharedArgs& a, const Walk& w) {
+    const int g0 = 8 * w.g;
     rows = min(8, a.G - g0);
-    head = hk * a.G + g0;
+    head = w.hk * a.G + g0;
     len = own_rows(a, w.b);
-    at = hk * a.R + w.b * a.G + g0;
+    at = w.hk * a.R + w.b * a.G + g0;
     row = w.b * a.H + head;
   }
 };
 
-// A warp's private ring of 2 KB slots for the own rows' tiles: lane 0 issues
-// the loads, every lane waits.
+// A warp's private ring of blocks for the own rows' tiles.
 struct OwnRing {
-  uint32_t base, bar;    // shared addresses: slot i at base + 2048 i, barrier i at bar + 8 i
+  uint32_t base, bar;    // shared addresses: slot i at base + kOwnBytes i, barrier i at bar + 8 i
   uint32_t issued, used; // tiles, both counted over the slots as 2 kOwnSlots states
   static __device__ __forceinline__ uint32_t step(uint32_t n) { return n + 1 == 2 * kOwnSlots ? 0u : n + 1; }
   static __device__ __forceinline__ uint32_t slot(uint32_t n) { return n < kOwnSlots ? n : n - kOwnSlots; }
   __device__ __forceinline__ void issue(const CUtensorMap* tm, int y, int z) {
-    if ((threadIdx.x & 31) == 0) {
-      const uint32_t i = slot(issued);
-      mbar_arrive_expect_tx(bar + 8 * i, 2048);
-      tma_load_3d(base + 2048 * i, tm, bar + 8 * i, 0, y, z);
-    }
+    const uint32_t i = slot(issued);
+    tma_load_3d_elect(base + kOwnBytes * i, tm, bar + 8 * i, kOwnBytes, 0, y, z);
     issued = step(issued);
   }
   // the oldest tile not yet used (its address), or 0 when the wait ran out
@@ -331,7 +325,7 @@ struct OwnRing {
     const uint32_t i = slot(used);
     const bool ok = mbar_wait_warp(bar + 8 * i, used >= kOwnSlots ? 1u : 0u, kRoleOwn);
     used = step(used);
-    return ok ? base + 2048 * i : 0u;
+    return ok ? base + kOwnBytes * i : 0u;
   }
   __device__ __forceinline__ void drain() {  // leave no copy in flight
     while (used != issued) wait();
@@ -365,92 +359,96 @@ __device__ __forceinline__ int key_of(int t, int i) {
 
 // ---- phase A of the own rows: scores and row max of the n blocks from w ----
 // A key past the sequence's last (in a started block) gets the lowest score,
-// whose table entry is 0.
-template <int D, bool kKSigned>
-__device__ __forceinline__ bool own_scores(const SharedArgs& a, OwnRing& ring, Walk w, int n) {
-  constexpr int kKeys = 2048 / D;      // 16 or 32
+// whose table entry is 0.  The next tile's fragments are read before this
+// one's scores are stored (with two own warps per scheduler the loop is bound by latency).
+template <int D>
+__device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRing& ring, Walk w, int n) {
+  constexpr int kKeys = kOwnBytes / D;
   constexpr int kSub = kKeys / 16;     // 16-key products per block
   constexpr int kCh = D / 64;          // 16-byte pieces of a row per thread: piece t (and t + 4)
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
-  const int groups = (a.G + 7) / 8, units = a.Hkv * groups;
-  if (n == 0) return true;
   Walk ld = w;
-  auto issue = [&]() { ring.issue(&a.tm_kc, ld.blk * kKeys, ld.b * a.Hkv + ld.u / groups); };
-  issue();
-  for (int i = 1; i < min(n, kOwnSlots); ++i) {
-    ld.next(a, kKeys, units);
-    issue();
-  }
-  uint4 q[kCh];
-  Unit x;
-  int32_t* sp = nullptr;
-  int32_t m[2];
-  auto enter = [&]() {
-    x.set(a, w, groups);
-    sp = a.scores + static_cast<size_t>(x.row + 2 * t) * a.ld_s;
+  int left = n;  // blocks not yet issued
+  auto issue = [&]() {
+    ring.issue(&a.tm_kc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk);
+    if (--left > 0) ld.next(a, kKeys);
+  };
+#pragma unroll 1
+  for (int i = 0; i < kOwnSlots; ++i)
+    if (left > 0) issue();
+  uint4 k[kSub][2][kCh];
+  bool fresh = false;  // k holds the tile of the next block
+  while (n > 0) {
+    Unit x;
+    x.set(a, w);
+    int32_t* sp = a.scores + static_cast<size_t>(x.row + 2 * t) * a.ld_s + score_at<D>(n8);
+    uint4 q[kCh];
 #pragma unroll
     for (int c = 0; c < kCh; ++c)
       q[c] = n8 < x.rows ? __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(x.row + n8) * D + 16 * t + 64 * c))
                          : make_uint4(0, 0, 0, 0);
-    m[0] = m[1] = INT_MIN;
-  };
-  auto leave = [&]() {
+    int32_t m[2] = {INT_MIN, INT_MIN};
+    const int run = min(n, w.nb - w.blk);  // blocks of this unit
+    n -= run;
+    // one more turn than blocks: each reads a tile, then works on the one read before it
+#pragma unroll 1
+    for (int i = fresh ? 1 : 0; i <= run; ++i) {
+      int32_t d[kSub][kCh][4];
+      if (i > 0) {
+#pragma unroll
+        for (int s = 0; s < kSub; ++s)
+#pragma unroll
+          for (int c = 0; c < kCh; ++c) {
+            d[s][c][0] = d[s][c][1] = d[s][c][2] = d[s][c][3] = 0;
+            mma16832(d[s][c], k_u8, k[s][0][c].x, k[s][1][c].x, k[s][0][c].y, k[s][1][c].y, q[c].x, q[c].y);
+            mma16832(d[s][c], k_u8, k[s][0][c].z, k[s][1][c].z, k[s][0][c].w, k[s][1][c].w, q[c].z, q[c].w);
+          }
+      }
+      if (i < run || n > 0) {
+        const uint32_t tile = ring.wait();
+        if (tile == 0) return false;
+#pragma unroll
+        for (int s = 0; s < kSub; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int c = 0; c < kCh; ++c) {
+              const int row = 16 * s + 8 * e + n8;  // the TMA's swizzle on the 16-byte piece
+              const int piece = D == 128 ? ((t + 4 * c) ^ (row & 7)) : (t ^ ((row >> 1) & 3));
+              k[s][e][c] = lds_u128(tile + row * D + 16 * piece);
+            }
+        __syncwarp();  // every lane has read the tile
+        if (left > 0) issue();
+      }
+      if (i == 0) continue;
+      // d[..][0], [1]: key n8, rows 2t and 2t + 1; [2], [3]: key n8 + 8
+      const int j0 = (w.blk + i - 1) * kKeys;
+#pragma unroll
+      for (int s = 0; s < kSub; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            int32_t v = d[s][0][2 * e + r];
+            if (kCh == 2) v += d[s][kCh - 1][2 * e + r];
+            if (j0 + 16 * s + 8 * e + n8 >= x.len) v = INT_MIN;
+            // key n8 + 8 is kept two positions after key n8 (score_at)
+            if (2 * t + r < x.rows) sp[static_cast<size_t>(r) * a.ld_s + j0 + 16 * s + 2 * e] = v;
+            m[r] = imax(m[r], v);
+          }
+    }
+    fresh = true;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       m[0] = imax(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
       m[1] = imax(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
     }
     if (n8 < 2 && 2 * t + n8 < x.rows) atomicMax(a.row_max + x.at + 2 * t + n8, bias(n8 ? m[1] : m[0]));
-  };
-  enter();
-  for (int i = 0; i < n; ++i) {
-    const uint32_t tile = ring.wait();
-    if (tile == 0) return false;
-    uint4 k[kSub][2][kCh];
-#pragma unroll
-    for (int s = 0; s < kSub; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          const int row = 16 * s + 8 * e + n8;  // the TMA's swizzle on the 16-byte piece
-          const int piece = D == 128 ? ((t + 4 * c) ^ (row & 7)) : (t ^ ((row >> 1) & 3));
-          k[s][e][c] = lds_u128(tile + row * D + 16 * piece);
-        }
-    __syncwarp();  // every lane has read the tile
-    if (i + kOwnSlots < n) {
-      ld.next(a, kKeys, units);
-      issue();
-    }
-#pragma unroll
-    for (int s = 0; s < kSub; ++s) {
-      int32_t d[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        mma16832<kKSigned, true>(d, k[s][0][c].x, k[s][1][c].x, k[s][0][c].y, k[s][1][c].y, q[c].x, q[c].y);
-        mma16832<kKSigned, true>(d, k[s][0][c].z, k[s][1][c].z, k[s][0][c].w, k[s][1][c].w, q[c].z, q[c].w);
-      }
-      // d[0], d[1]: key n8, rows 2t and 2t + 1; d[2], d[3]: key n8 + 8
-      const int j0 = w.blk * kKeys + 16 * s;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        int32_t* dst = sp + j0 + score_at<D>(8 * e + n8);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int32_t v = j0 + 8 * e + n8 < x.len ? d[2 * e + r] : INT_MIN;
-          if (2 * t + r < x.rows) dst[static_cast<size_t>(r) * a.ld_s] = v;
-          m[r] = imax(m[r], v);
-        }
-      }
-    }
-    if (i + 1 < n) {
-      const bool moves = w.blk + 1 == w.nb;
-      if (moves) leave();
-      w.next(a, kKeys, units);
-      if (moves) enter();
+    if (n > 0) {
+      w.blk += run - 1;
+      w.next(a, kKeys);
     }
   }
-  leave();
   return true;
 }
 
@@ -472,117 +470,165 @@ struct RowIndex {
 };
 
 // ---- phase B of the own rows: Z and the index bytes of the same blocks ----
-// Thread (n8, t): query row n8, four scores of each 16-key block; four
-// blocks' loads in flight.
+// Thread t of four takes four scores of a 16-key block; the eight lane groups
+// take the unit's rows, and with fewer than eight rows several blocks.  Two
+// batches of loads in flight.
 template <int D>
 __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDev* hp_s, const uint32_t* lut_s, Walk w,
                                          int n) {
-  constexpr int kKeys = 2048 / D;
+  constexpr int kKeys = kOwnBytes / D;
   constexpr int kSub = kKeys / 16;
-  constexpr int kBatch = 4;  // 16-key blocks
+  constexpr int kBatch = 4;
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
-  const int groups = (a.G + 7) / 8, units = a.Hkv * groups;
   while (n > 0) {
     const int run = min(n, w.nb - w.blk);  // blocks of this unit
     Unit x;
-    x.set(a, w, groups);
-    const int mine = min(n8, x.rows - 1);
-    const int s0 = w.blk * kSub, s1 = min((w.blk + run) * kSub, (x.len + 15) / 16);  // started 16-key blocks
+    x.set(a, w);
+    const int rp = x.rows > 4 ? 8 : x.rows > 2 ? 4 : x.rows;  // lane groups per block
+    const int par = 8 / rp;                                   // blocks side by side
+    const int mine = min(n8 % rp, x.rows - 1);
+    const bool live = n8 % rp < x.rows;
+    const int s0 = w.blk * kSub + n8 / rp, s1 = min((w.blk + run) * kSub, (x.len + 15) / 16);  // started blocks
     const size_t row = static_cast<size_t>(x.row + mine) * a.ld_s + 4 * t;
     const int4* sp = reinterpret_cast<const int4*>(a.scores + row);
     uint32_t* ip = a.index + row / 4;
-    int4 v[kBatch];
-    auto load = [&](int s) {
+    auto load = [&](int4 (&v)[kBatch], int s) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        v[k] = s + k < s1 ? sp[4 * (s + k)] : make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
+        v[k] = s + k * par < s1 ? sp[4 * (s + k * par)] : make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
     };
-    load(s0);
+    int4 v[kBatch], nx[kBatch];
+    load(v, s0);
     const HeadParamsDev hp = hp_s[a.per_head ? x.head + mine : 0];
     const uint32_t* lut = lut_s + 32 * hp.lut;
     RowIndex index;
     index.set(hp, unbias(__ldcg(a.row_max + x.at + mine)));
     uint32_t z = 0;
-    for (int s = s0; s < s1; s += kBatch) {
-      uint32_t word[kBatch];
+    for (int s = s0; s < s1; s += kBatch * par) {
+      load(nx, s + kBatch * par);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const uint32_t i0 = index(v[k].x), i1 = index(v[k].y), i2 = index(v[k].z), i3 = index(v[k].w);
         z += (lut[i0] + lut[i1]) + (lut[i2] + lut[i3]);
-        word[k] = prefill::pack4(i0, i1, i2, i3);
-      }
-      if (s + kBatch < s1) load(s + kBatch);
-      if (n8 < x.rows) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (s + k < s1) ip[4 * (s + k)] = word[k];
+        if (live && s + k * par < s1) ip[4 * (s + k * par)] = prefill::pack4(i0, i1, i2, i3);
+        v[k] = nx[k];
       }
     }
+    __syncwarp();
     z += __shfl_xor_sync(0xffffffffu, z, 1);
     z += __shfl_xor_sync(0xffffffffu, z, 2);
+    for (int o = 4 * rp; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     if (t == 0 && n8 < x.rows) atomicAdd(a.row_z + x.at + n8, static_cast<int32_t>(z));
     n -= run;
     if (n > 0) {
       w.blk += run - 1;
-      w.next(a, kKeys, units);
+      w.next(a, kKeys);
     }
   }
 }
 
 // First V tiles of the share into the ring: they wait for nothing, so they
-// start before the barrier that phase C waits for.  Leaves `ld` at the last one.
+// start before the barrier that phase C waits for.  Leaves `ld` at the next one.
 template <int D>
-__device__ __forceinline__ void own_pv_start(const SharedArgs& a, OwnRing& ring, Walk& ld, int n) {
-  constexpr int kKeys = 2048 / D;
-  const int groups = (a.G + 7) / 8, units = a.Hkv * groups;
-  for (int i = 0; i < min(n, kOwnSlots); ++i) {
-    if (i > 0) ld.next(a, kKeys, units);
-    ring.issue(&a.tm_vc, ld.blk * kKeys, ld.b * a.Hkv + ld.u / groups);
+__device__ __forceinline__ int own_pv_start(const SharedArgs& a, OwnRing& ring, Walk& ld, int n) {
+#pragma unroll 1
+  for (int i = 0; i < kOwnSlots && n > 0; ++i) {
+    ring.issue(&a.tm_vc, ld.blk * (kOwnBytes / D), ld.b * a.Hkv + ld.hk);
+    if (--n > 0) ld.next(a, kOwnBytes / D);
   }
+  return n;  // blocks not yet issued
 }
 
 // ---- phase C of the own rows: P.V of the same blocks ----
 // A = V^T: the thread (n8, t) reads D / 8 channels (from D / 8 n8) of the four
 // keys key_of(t, i), which make a fragment word per channel.  B = P: query row
-// n8, the same keys.
-template <int D, bool kVSigned>
-__device__ __forceinline__ bool own_pv(const SharedArgs& a, OwnRing& ring, const HeadParamsDev* hp_s,
-                                       const uint32_t* lut_s, Walk w, Walk ld, int n) {
-  constexpr int kKeys = 2048 / D;
+// n8, the same keys.  P of the next block is made while this one's V is read.
+template <int D>
+__device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& ring, const HeadParamsDev* hp_s,
+                                       const uint32_t* lut_s, Walk w, Walk ld, int left, int n) {
+  constexpr int kKeys = kOwnBytes / D;
   constexpr int kSub = kKeys / 16;
   constexpr int kWords = D / 32;  // 4-channel words of a row per thread
-  constexpr int kAhead = 2;       // blocks whose index words are in flight
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
-  const int groups = (a.G + 7) / 8, units = a.Hkv * groups;
-  if (n == 0) return true;
-  Unit x;
-  const uint32_t* ip = nullptr;
-  uint32_t lut = 0;  // shared address
-  uint32_t R = 0;  // < 2^25: Z is at least 2^15
-  uint32_t psum = 0;
-  int32_t o[D / 16][4];
-  uint32_t ix[kAhead + 1][kSub];  // index words of this block and the next ones of its unit
-  auto load_index = [&](uint32_t (&v)[kSub], int blk) {
-#pragma unroll
-    for (int s = 0; s < kSub; ++s)
-      v[s] = 16 * (blk * kSub + s) < x.len ? ip[4 * (blk * kSub + s)] : 0x1F1F1F1Fu;
-  };
-  auto enter = [&]() {
-    x.set(a, w, groups);
+  while (n > 0) {
+    Unit x;
+    x.set(a, w);
     const int mine = min(n8, x.rows - 1);
-    ip = a.index + static_cast<size_t>(x.row + mine) * (a.ld_s / 4) + t;
+    const uint32_t* ip = a.index + static_cast<size_t>(x.row + mine) * (a.ld_s / 4) + t;
+    uint32_t ix[kSub], p[kSub];  // index words of the block after next, P of the next
+    auto load_index = [&](int blk) {
 #pragma unroll
-    for (int k = 0; k <= kAhead; ++k) load_index(ix[k], w.blk + k);
-    R = static_cast<uint32_t>(exact_R(__ldcg(a.row_z + x.at + mine)));
-    lut = smem_u32(lut_s) + 128 * hp_s[a.per_head ? x.head + mine : 0].lut;
-    psum = 0;
+      for (int s = 0; s < kSub; ++s)
+        ix[s] = 16 * (blk * kSub + s) < x.len ? ip[4 * (blk * kSub + s)] : 0x1F1F1F1Fu;
+    };
+    load_index(w.blk);
+    const uint32_t R = static_cast<uint32_t>(exact_R(__ldcg(a.row_z + x.at + mine)));  // < 2^25: Z >= 2^15
+    const uint32_t lut = smem_u32(lut_s) + 128 * hp_s[a.per_head ? x.head + mine : 0].lut;
+    uint32_t psum = 0;
+    int32_t o[D / 16][4];
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[c][i] = 0;
-  };
-  auto leave = [&]() {
-    if (a.v_u8) {
+    const int run = min(n, w.nb - w.blk);  // blocks of this unit
+    n -= run;
+    // one more turn than blocks: each makes the P of its block, after the V work on the one before
+#pragma unroll 1
+    for (int i = 0; i <= run; ++i) {
+      if (i > 0) {
+        const uint32_t tile = ring.wait();
+        if (tile == 0) return false;
+#pragma unroll
+        for (int s = 0; s < kSub; ++s) {
+          uint32_t v[4][kWords];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 16 * s + key_of<D>(t, e);  // the TMA's swizzle on the 16-byte piece
+            if constexpr (D == 128) {
+              const uint4 y = lds_u128(tile + row * 128 + 16 * (n8 ^ (row & 7)));
+              v[e][0] = y.x;
+              v[e][1] = y.y;
+              v[e][2] = y.z;
+              v[e][3] = y.w;
+            } else {
+              const uint2 y = lds_u64(tile + row * 64 + 16 * ((n8 >> 1) ^ ((row >> 1) & 3)) + 8 * (n8 & 1));
+              v[e][0] = y.x;
+              v[e][1] = y.y;
+            }
+          }
+          if (s == kSub - 1) {
+            __syncwarp();  // every lane has read the tile
+            if (left > 0) {
+              ring.issue(&a.tm_vc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk);
+              if (--left > 0) ld.next(a, kKeys);
+            }
+          }
+          // bytes (key, channel c) -> word c holds four keys of channel c
+#pragma unroll
+          for (int q = 0; q < kWords; ++q) {
+            const uint32_t ab_lo = __byte_perm(v[0][q], v[1][q], 0x5140), ab_hi = __byte_perm(v[0][q], v[1][q], 0x7362);
+            const uint32_t cd_lo = __byte_perm(v[2][q], v[3][q], 0x5140), cd_hi = __byte_perm(v[2][q], v[3][q], 0x7362);
+            mma16816(o[2 * q], v_u8, __byte_perm(ab_lo, cd_lo, 0x5410), __byte_perm(ab_lo, cd_lo, 0x7632), p[s]);
+            mma16816(o[2 * q + 1], v_u8, __byte_perm(ab_hi, cd_hi, 0x5410), __byte_perm(ab_hi, cd_hi, 0x7632), p[s]);
+          }
+        }
+      }
+      if (i < run) {
+        // P (0 for rows the unit does not have)
+#pragma unroll
+        for (int s = 0; s < kSub; ++s) {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            b[e] = static_cast<uint32_t>(
+                (static_cast<unsigned long long>(lds_u32(lut + 4 * ((ix[s] >> (8 * e)) & 255u))) * R + (1ull << 31)) >> 32);
+          p[s] = n8 < x.rows ? prefill::pack4(b[0], b[1], b[2], b[3]) : 0u;
+          psum = __dp4a(p[s], 0x01010101u, psum);
+        }
+        load_index(w.blk + i + 1);
+      }
+    }
+    if (v_u8) {
       psum += __shfl_xor_sync(0xffffffffu, psum, 1);
       psum += __shfl_xor_sync(0xffffffffu, psum, 2);
       if (t == 0 && n8 < x.rows) atomicAdd(a.row_p + x.at + n8, static_cast<int32_t>(psum));
@@ -597,73 +643,11 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, OwnRing& ring, const
           red_add4(dst + 2 * c, static_cast<float>(o[c][r]), static_cast<float>(o[c][2 + r]),
                    static_cast<float>(o[c + 1][r]), static_cast<float>(o[c + 1][2 + r]));
       }
-  };
-  enter();
-  for (int i = 0; i < n; ++i) {
-    // P of this block (0 for rows the unit does not have)
-    uint32_t p[kSub];
-#pragma unroll
-    for (int s = 0; s < kSub; ++s) {
-      uint32_t b[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        b[e] = static_cast<uint32_t>(
-            (static_cast<unsigned long long>(lds_u32(lut + 4 * ((ix[0][s] >> (8 * e)) & 255u))) * R + (1ull << 31)) >> 32);
-      p[s] = n8 < x.rows ? prefill::pack4(b[0], b[1], b[2], b[3]) : 0u;
-      psum = __dp4a(p[s], 0x01010101u, psum);
-    }
-    const uint32_t tile = ring.wait();
-    if (tile == 0) return false;
-#pragma unroll
-    for (int s = 0; s < kSub; ++s) {
-      uint32_t v[4][kWords];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = 16 * s + key_of<D>(t, e);  // the TMA's swizzle on the 16-byte piece
-        if constexpr (D == 128) {
-          const uint4 y = lds_u128(tile + row * 128 + 16 * (n8 ^ (row & 7)));
-          v[e][0] = y.x;
-          v[e][1] = y.y;
-          v[e][2] = y.z;
-          v[e][3] = y.w;
-        } else {
-          const uint2 y = lds_u64(tile + row * 64 + 16 * ((n8 >> 1) ^ ((row >> 1) & 3)) + 8 * (n8 & 1));
-          v[e][0] = y.x;
-          v[e][1] = y.y;
-        }
-      }
-      if (s == kSub - 1) {
-        __syncwarp();  // every lane has read the tile
-        if (i + kOwnSlots < n) {
-          ld.next(a, kKeys, units);
-          ring.issue(&a.tm_vc, ld.blk * kKeys, ld.b * a.Hkv + ld.u / groups);
-        }
-      }
-      // bytes (key, channel c) -> word c holds four keys of channel c
-#pragma unroll
-      for (int q = 0; q < kWords; ++q) {
-        const uint32_t ab_lo = __byte_perm(v[0][q], v[1][q], 0x5140), ab_hi = __byte_perm(v[0][q], v[1][q], 0x7362);
-        const uint32_t cd_lo = __byte_perm(v[2][q], v[3][q], 0x5140), cd_hi = __byte_perm(v[2][q], v[3][q], 0x7362);
-        mma16816<kVSigned>(o[2 * q], __byte_perm(ab_lo, cd_lo, 0x5410), __byte_perm(ab_lo, cd_lo, 0x7632), p[s]);
-        mma16816<kVSigned>(o[2 * q + 1], __byte_perm(ab_hi, cd_hi, 0x5410), __byte_perm(ab_hi, cd_hi, 0x7632), p[s]);
-      }
-    }
-    if (i + 1 < n) {
-      const bool moves = w.blk + 1 == w.nb;
-      if (moves) leave();
-      w.next(a, kKeys, units);
-      if (moves) {
-        enter();
-      } else {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-          for (int s = 0; s < kSub; ++s) ix[k][s] = ix[k + 1][s];
-        load_index(ix[kAhead], w.blk + kAhead);
-      }
+    if (n > 0) {
+      w.blk += run - 1;
+      w.next(a, kKeys);
     }
   }
-  leave();
   return true;
 }
 
@@ -703,7 +687,8 @@ __device__ __forceinline__ void finish(const SharedArgs& a, const HeadParamsDev*
   }
 }
 
-template <int D>
+// ZP: the instance for K or V codes with zero-points (u8); the other takes int8 only.
+template <int D, bool ZP>
 __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_constant__ SharedArgs args) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -727,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     if (tid == 0) atomicOr(&g_device_error, kErrTimeout);
     return;
   }
+  const bool k_u8 = ZP && args.k_u8, v_u8 = ZP && args.v_u8;
   const int F = args.fold;
   const int RF = kBM / F;       // lanes per fold
   const int psets = kPBufs / F; // sets of F P buffers
@@ -786,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     bar_red_and(kNbBoth, 32 * (kSoftWarps + kOwnWarps), true);
     return *verdict != 0u;
   };
-  constexpr int kFinishers = 32 * (kSoftWarps + kOwnWarps);
+  bool complete = false;  // softmax and own warps: acc holds every sum
   constexpr int kPieces = D / 16;  // of a row
   // piece i of the query rows of a segment (16-byte pieces, row by row)
   auto q_piece = [&](const Segment& sg, int i) {
@@ -1008,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
                 for (int b = 0; b < 4; ++b) p[b] = lds_u32(kb[b] * 512u + prow + (b & 1) * C::kTabBytes);
                 pw[q] = (p[0] + p[1]) + ((p[2] + p[3]) << 16);
               }
-              if (args.v_u8) {
+              if (v_u8) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) psum = __dp4a(pw[q], 0x01010101u, psum);
               }
@@ -1052,7 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           t += sg.n;
           if (!soft_sync(ok)) { ok = false; break; }
         }
-        if (grid_sync(2, ok)) finish<D>(args, hp_s, blockIdx.x * kFinishers + tid, gridDim.x * kFinishers);
+        complete = grid_sync(2, ok);
       }
     }
   } else if (warp >= kOwnWarp0) {
@@ -1073,22 +1059,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       }
     Walk w;
     // neighbouring shares on different CTAs
-    const int n = args.Lmax > 0 ? w.share(args, 2048 / D, args.Hkv * ((args.G + 7) / 8), ow * gridDim.x + blockIdx.x,
-                                          kOwnWarps * gridDim.x)
+    const int n = args.Lmax > 0 ? w.share(args, kOwnBytes / D, ow * gridDim.x + blockIdx.x, kOwnWarps * gridDim.x)
                                 : 0;
-    OwnRing ring{s_base + C::kOffOwn + 2048u * kOwnSlots * ow, bar(kBarOwn + kOwnSlots * ow), 0u, 0u};
+    OwnRing ring{s_base + C::kOffOwn + kOwnBytes * kOwnSlots * ow, bar(kBarOwn + kOwnSlots * ow), 0u, 0u};
     quant::griddep_wait();
-    bool ok = args.k_u8 ? own_scores<D, false>(args, ring, w, n) : own_scores<D, true>(args, ring, w, n);
+    bool ok = own_scores<D>(args, k_u8, ring, w, n);
     if ((ok = grid_sync(0, ok))) {
       Walk ld = w;
-      own_pv_start<D>(args, ring, ld, n);
+      const int left = own_pv_start<D>(args, ring, ld, n);
       own_sums<D>(args, hp_s, lut_s, w, n);
       if ((ok = grid_sync(1, true))) {
-        ok = args.v_u8 ? own_pv<D, false>(args, ring, hp_s, lut_s, w, ld, n)
-                       : own_pv<D, true>(args, ring, hp_s, lut_s, w, ld, n);
-        if (grid_sync(2, ok))
-          finish<D>(args, hp_s, blockIdx.x * kFinishers + 32 * kSoftWarps + tid - 32 * kOwnWarp0,
-                    gridDim.x * kFinishers);
+        ok = own_pv<D>(args, v_u8, ring, hp_s, lut_s, w, ld, left, n);
+        complete = grid_sync(2, ok);
       }
     }
     ring.drain();
@@ -1119,29 +1101,27 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           }
         }
       };
-      for (int phase = 0; phase < 2; ++phase)
+      // in the order the MMA warp takes them
+#pragma unroll 1
+      for (int phase = 0; phase < 3; ++phase)
         for (int t = t0; t < t1 && ok;) {
           const Segment sg = segment_at(args, t, t1);
-          for (int j = 0; j < sg.n; ++j) load(&args.tm_k, sg.j0 + j, sg.hk);
+          const int turns = 2 * sg.n + (phase == 2 ? 4 : 0);  // K of tile e, V of tile e - 2
+#pragma unroll 1
+          for (int y = 0; y < turns; ++y) {
+            const int j = (y >> 1) - ((y & 1) ? 2 : 0);
+            if (j < 0 || j >= sg.n || ((y & 1) && phase < 2)) continue;
+            load((y & 1) ? &args.tm_v : &args.tm_k, sg.j0 + j, sg.hk);
+          }
           t += sg.n;
         }
-      for (int t = t0; t < t1 && ok;) {
-        const Segment sg = segment_at(args, t, t1);
-        load(&args.tm_k, sg.j0, sg.hk);
-        if (sg.n > 1) load(&args.tm_k, sg.j0 + 1, sg.hk);
-        for (int j = 0; j < sg.n; ++j) {
-          if (j + 2 < sg.n) load(&args.tm_k, sg.j0 + j + 2, sg.hk);
-          load(&args.tm_v, sg.j0 + j, sg.hk);
-        }
-        t += sg.n;
-      }
       if (mine > 0) mbar_wait(bar_kv_full(slot), (mine - 1) & 1, kRoleProducer);  // no copy left in flight
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ============================= MMA issuer =============================
-    const uint32_t idesc_qk = idesc_i8(kBM, kBN, 1, args.k_u8 ? 0u : 1u, 0);
-    const uint32_t idesc_pv = idesc_i8(kBM, D, 0, args.v_u8 ? 0u : 1u, 1);
+    const uint32_t idesc_qk = idesc_i8(kBM, kBN, 1, k_u8 ? 0u : 1u, 0);
+    const uint32_t idesc_pv = idesc_i8(kBM, D, 0, v_u8 ? 0u : 1u, 1);
     const uint64_t kv_desc0 = smem_desc(sKV, 16, C::kSBO, C::kSwizzle);
     const uint64_t q_desc0 = smem_desc(s_base + C::kOffQ, 16, C::kSBO, C::kSwizzle);
     constexpr uint32_t kSlotDesc = C::kTileBytes >> 4;
@@ -1191,66 +1171,65 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         const uint32_t qb = nq & 1;
         if (!mbar_wait_warp(bar(kBarQFull + qb), q_stays ? 0u : (nq >> 1) & 1, kRoleMma)) { ok = false; break; }
         const uint64_t q_desc = q_desc0 + ((static_cast<uint32_t>(kBM - RF + kBM * qb) * D) >> 4);
-        // S of tile j: the queries in the lanes of fold x against key tile x
-        auto issue_qk = [&](int j) {
-          if (!ok) return;
-          const uint32_t buf = sc & 1;
-          const int nf = folds_at(args, j);
-          if (!wait_tiles(nf, bar(kBarSEmpty + buf), ((sc >> 1) & 1) ^ 1, 0u, 0u)) {
-            ok = false;
-            return;
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            uint32_t sl = slot;
-            for (int x = 0; x < nf; ++x, sl = step(sl)) {
-              const uint64_t k_desc = kv_desc0 + sl * kSlotDesc;
-              const uint64_t a_desc = q_desc - ((static_cast<uint32_t>(x * RF) * D) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                mma_i8_ss(tmem + kColS + buf * kBN, a_desc + 2 * kk, k_desc + 2 * kk, idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
-              mma_commit(bar_kv_empty(sl));
-            }
-            mma_commit(bar(kBarSFull + buf));
-          }
-          __syncwarp();
-          advance(nf);
-          ++sc;
-        };
-        if (phase < 2) {
-          for (int j = 0; j < sg.n; ++j) issue_qk(sg.j0 + j);
-        } else {
-          issue_qk(sg.j0);
-          if (sg.n > 1) issue_qk(sg.j0 + 1);
-          for (int j = 0; ok && j < sg.n; ++j, ++pc) {
-            if (j + 2 < sg.n) issue_qk(sg.j0 + j + 2);
-            if (!ok) break;
-            const uint32_t set = pc & (psets - 1);
-            const int nf = folds_at(args, sg.j0 + j);
-            // the first P.V of a segment: O of the previous one has been read
-            if (!wait_tiles(nf, bar(kBarPFull + set), (pc / psets) & 1, j == 0 ? bar(kBarOEmpty) : 0u, (no & 1) ^ 1)) {
+        // S of tile e (the queries in the lanes of fold x against key tile x),
+        // then, in phase C, P.V of tile e - 2: S of the next two tiles is
+        // always issued before the P.V that waits for the softmax
+        const int turns = sg.n + (phase == 2 ? 2 : 0);
+#pragma unroll 1
+        for (int e = 0; ok && e < turns; ++e) {
+          if (e < sg.n) {
+            const uint32_t buf = sc & 1;
+            const int nf = folds_at(args, sg.j0 + e);
+            if (!wait_tiles(nf, bar(kBarSEmpty + buf), ((sc >> 1) & 1) ^ 1, 0u, 0u)) {
               ok = false;
               break;
             }
             tc_fence_after();
             if (elect_one()) {
               uint32_t sl = slot;
+#pragma unroll 1
               for (int x = 0; x < nf; ++x, sl = step(sl)) {
-                const uint64_t v_desc = kv_desc0 + sl * kSlotDesc;
+                const uint64_t k_desc = kv_desc0 + sl * kSlotDesc;
+                const uint64_t a_desc = q_desc - ((static_cast<uint32_t>(x * RF) * D) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kBN / 32; ++kk)
-                  mma_i8_ts(tmem + kColO, tmem + kColP + (set * F + x) * 32 + kk * 8, v_desc + ((32u * D * kk) >> 4),
-                            idesc_pv, (j > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < D / 32; ++kk)
+                  mma_i8_ss(tmem + kColS + buf * kBN, a_desc + 2 * kk, k_desc + 2 * kk, idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(bar_kv_empty(sl));
               }
-              mma_commit(bar(kBarPEmpty + set));
+              mma_commit(bar(kBarSFull + buf));
             }
             __syncwarp();
             advance(nf);
+            ++sc;
           }
-          if (!ok) break;
-          mma_commit_elect(bar(kBarOFull));
-          ++no;
+          const int j = e - 2;
+          if (phase < 2 || j < 0) continue;
+          const uint32_t set = pc & (psets - 1);
+          const int nf = folds_at(args, sg.j0 + j);
+          // the first P.V of a segment: O of the previous one has been read
+          if (!wait_tiles(nf, bar(kBarPFull + set), (pc / psets) & 1, j == 0 ? bar(kBarOEmpty) : 0u, (no & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            uint32_t sl = slot;
+#pragma unroll 1
+            for (int x = 0; x < nf; ++x, sl = step(sl)) {
+              const uint64_t v_desc = kv_desc0 + sl * kSlotDesc;
+#pragma unroll
+              for (int kk = 0; kk < kBN / 32; ++kk)
+                mma_i8_ts(tmem + kColO, tmem + kColP + (set * F + x) * 32 + kk * 8, v_desc + ((32u * D * kk) >> 4),
+                          idesc_pv, (j > 0 || x > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(bar_kv_empty(sl));
+            }
+            mma_commit(bar(kBarPEmpty + set));
+            if (j == sg.n - 1) mma_commit(bar(kBarOFull));
+          }
+          __syncwarp();
+          advance(nf);
+          ++pc;
+          if (j == sg.n - 1) ++no;
         }
         if (!ok) break;
         if (!q_stays) mma_commit_elect(bar(kBarQEmpty + qb));
@@ -1291,6 +1270,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     }
   }
 
+  if (complete) {
+    constexpr int kFinishers = 32 * (kSoftWarps + kOwnWarps);
+    finish<D>(args, hp_s, blockIdx.x * kFinishers + (warp < kSoftWarps ? tid : tid - 32 * (kOwnWarp0 - kSoftWarps)),
+              gridDim.x * kFinishers);
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
