@@ -37,9 +37,8 @@
 // eight query rows per K / V row.  Each of the own warps takes an equal
 // consecutive share of all blocks of own rows (4 KB each) and streams it through
 // a ring of its own TMA tiles: 64 KB in flight per SM, no registers held by loads, no
-// barrier shared by warps.  The products are m16n8k32 and m16n8k16 integer MMAs, keys or
-// channels on the 16 side and the grouped heads on the 8 side; the contraction
-// order is free, so a thread's consecutive bytes serve as its fragments.  Scores
+// barrier shared by warps.  The products are m16n8k32 integer MMAs, keys or channels on
+// the 16 side and the grouped heads on the 8 side.  Scores
 // (4 bytes per key and head), and from phase B on their table indices (one
 // byte), wait in the workspace; a warp reads back what it wrote itself.
 #pragma once
@@ -191,14 +190,15 @@ __device__ __forceinline__ void mma16832(int32_t (&c)[4], bool a_u8, uint32_t a0
     asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// D[16 x 8] += A[16 x 16] B[16 x 8]: A s8 or u8 (V), B u8 (P).
-__device__ __forceinline__ void mma16816(int32_t (&c)[4], bool a_u8, uint32_t a0, uint32_t a1, uint32_t b0) {
+// The same with A s8 or u8 (V), B u8 (P).
+__device__ __forceinline__ void mma16832_pv(int32_t (&c)[4], bool a_u8, uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
   if (a_u8)
-    asm("mma.sync.aligned.m16n8k16.row.col.s32.u8.u8.s32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm("mma.sync.aligned.m16n8k16.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(b0));
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Own rows of a sequence; 0 for a length out of range (its output is skipped).
@@ -224,52 +224,47 @@ struct Walk {
     for (int i = lane; i < a.B; i += 32) total += cost(blocks(i));
     total = __reduce_add_sync(0xffffffffu, total) * units;
     const int each = total / warps, more = total - each * warps;
-    int p[2];  // the share's ends, in units of cost from the current sequences on
-    p[0] = each * w + min(w, more);
-    p[1] = p[0] + each + (w < more ? 1 : 0);
-    int at[2] = {0, 0};  // blocks before them
-    bool found[2] = {false, false};
+    const int first = each * w + min(w, more);
+    int n = 0, u = 0;
     b = hk = g = blk = nb = 0;
-    int u = 0;
-    for (int b0 = 0; b0 < a.B && !found[1]; b0 += 32) {
-      const int mine = blocks(b0 + lane);
-      int c = cost(mine), n = mine;  // sums up to and with this lane's sequence
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int c_up = __shfl_up_sync(0xffffffffu, c, o), n_up = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) {
-          c += c_up;
-          n += n_up;
+    // the share's end, then its start: the blocks before them, and where they are
+#pragma unroll 1
+    for (int e = 1; e >= 0; --e) {
+      int p = e ? first + each + (w < more ? 1 : 0) : first;  // in units of cost from sequence b0 on
+      int before = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int mine = blocks(b0 + lane);
+        int c = cost(mine), k = mine;  // sums up to and with this lane's sequence
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const int c_up = __shfl_up_sync(0xffffffffu, c, o), k_up = __shfl_up_sync(0xffffffffu, k, o);
+          if (lane >= o) {
+            c += c_up;
+            k += k_up;
+          }
         }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (found[e]) continue;
-        const uint32_t past = __ballot_sync(0xffffffffu, c * units > p[e]);
+        const uint32_t past = __ballot_sync(0xffffffffu, c * units > p);
         if (past) {
           const int l = __ffs(past) - 1;
-          const int k = __shfl_sync(0xffffffffu, mine, l);
-          const int q = p[e] - (__shfl_sync(0xffffffffu, c, l) - cost(k)) * units;  // within sequence b0 + l
-          int v = q / cost(k), o = q - v * cost(k);
-          if (o >= k) {  // between two units: the next one's first block
-            ++v;
-            o = 0;
+          nb = __shfl_sync(0xffffffffu, mine, l);
+          b = b0 + l;
+          const int q = p - (__shfl_sync(0xffffffffu, c, l) - cost(nb)) * units;  // within sequence b
+          u = q / cost(nb);
+          blk = q - u * cost(nb);
+          if (blk >= nb) {  // between two units: the next one's first block
+            ++u;
+            blk = 0;
           }
-          at[e] += (__shfl_sync(0xffffffffu, n, l) - k) * units + v * k + o;
-          found[e] = true;
-          if (e == 0) {
-            b = b0 + l;
-            u = v;
-            blk = o;
-            nb = k;
-          }
-        } else {
-          at[e] += __shfl_sync(0xffffffffu, n, 31) * units;
-          p[e] -= __shfl_sync(0xffffffffu, c, 31) * units;
+          before += (__shfl_sync(0xffffffffu, k, l) - nb) * units + u * nb + blk;
+          break;
         }
+        before += __shfl_sync(0xffffffffu, k, 31) * units;
+        p -= __shfl_sync(0xffffffffu, c, 31) * units;
       }
+      n = e ? before : n - before;
     }
-    const int n = at[1] - at[0];
+    if (n == 0) return 0;
     const bool over = u == units;  // the first block is the next sequence's
     if (over) {
       --u;
@@ -277,7 +272,7 @@ struct Walk {
     }
     hk = u / groups;
     g = u - hk * groups;
-    if (n > 0 && over) next(a, keys);
+    if (over) next(a, keys);
     return n;
   }
   // to the next block (there is one)
@@ -332,40 +327,40 @@ struct OwnRing {
   }
 };
 
-__device__ __forceinline__ uint4 lds_u128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+// Four 8 x 8 matrices of 16-bit elements, that is 8 rows of 16 bytes each:
+// lane 8 i + j gives the address of row j of matrix i; thread (n8, t) gets bytes
+// 4 t .. 4 t + 3 of row n8.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
-__device__ __forceinline__ uint2 lds_u64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
+// Two 16 x 16 matrices of bytes, transposed: lane 16 i + j gives the address
+// of row j of matrix i; thread (n8, t) gets of column n8 (r[2 i]) and n8 + 8 (r[2 i + 1]) the
+// rows 4 t .. 4 t + 3.
+__device__ __forceinline__ void ldmatrix2_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
-
-// Where the score of key kk of a 16-key block is kept: thread t of phases B
-// and C takes the keys key_of(t, 0 .. 3), whose indices make one word.  Its V
-// rows lie in other banks than the other threads' under the tile's swizzle (the
-// 16-byte piece is XORed with row bits 0-2 for D = 128, 1-2 for D = 64).
+// Shared address of 16-byte piece c of row r of a swizzled tile of D-byte rows.
 template <int D>
-__device__ __forceinline__ int score_at(int kk) {
-  return D == 128 ? ((kk & 6) << 1) | ((kk & 8) >> 2) | (kk & 1)
-                  : ((kk & 1) << 2) | ((kk & 4) << 1) | ((kk & 8) >> 2) | ((kk & 2) >> 1);
-}
-template <int D>
-__device__ __forceinline__ int key_of(int t, int i) {
-  return D == 128 ? 2 * t + (i & 1) + 8 * (i >> 1) : (t & 1) + 4 * (t >> 1) + 2 * (i & 1) + 8 * (i >> 1);
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int c) {
+  return tile + r * D + 16 * (D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3)));
 }
 
 // ---- phase A of the own rows: scores and row max of the n blocks from w ----
-// A key past the sequence's last (in a started block) gets the lowest score,
-// whose table entry is 0.  The next tile's fragments are read before this
-// one's scores are stored (with two own warps per scheduler the loop is bound by latency).
+// A = K: sixteen keys by 32 channels per product; B: the unit's queries.  A key
+// past the sequence's last (in a started 16-key step) gets the lowest score, whose table
+// entry is 0.  The next step's fragments are read before this one's scores
+// are stored (with two own warps per scheduler the loop is bound by latency).
 template <int D>
 __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRing& ring, Walk w, int n) {
   constexpr int kKeys = kOwnBytes / D;
-  constexpr int kSub = kKeys / 16;     // 16-key products per block
-  constexpr int kCh = D / 64;          // 16-byte pieces of a row per thread: piece t (and t + 4)
+  constexpr int kSub = kKeys / 16;     // 16-key steps per block
+  constexpr int kK = D / 32;           // products per step
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
   Walk ld = w;
   int left = n;  // blocks not yet issued
@@ -376,68 +371,66 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
 #pragma unroll 1
   for (int i = 0; i < kOwnSlots; ++i)
     if (left > 0) issue();
-  uint4 k[kSub][2][kCh];
-  bool fresh = false;  // k holds the tile of the next block
+  uint32_t k[kK][4];  // fragments of the next step
+  uint32_t tile = 0;
+  bool fresh = false;  // k holds them
+  auto read = [&](int s) {
+#pragma unroll
+    for (int c = 0; c < kK; ++c) ldmatrix4(k[c], tile_at<D>(tile, 16 * s + (lane & 15), 2 * c + (lane >> 4)));
+  };
   while (n > 0) {
     Unit x;
     x.set(a, w);
-    int32_t* sp = a.scores + static_cast<size_t>(x.row + 2 * t) * a.ld_s + score_at<D>(n8);
-    uint4 q[kCh];
+    int32_t* sp = a.scores + static_cast<size_t>(x.row + 2 * t) * a.ld_s + n8;
+    uint32_t q[kK][2];
+    {
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(a.q + static_cast<size_t>(x.row + min(n8, x.rows - 1)) * D) + t;
 #pragma unroll
-    for (int c = 0; c < kCh; ++c)
-      q[c] = n8 < x.rows ? __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(x.row + n8) * D + 16 * t + 64 * c))
-                         : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < kK; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) q[c][i] = __ldg(qp + 8 * c + 4 * i);  // rows past the unit's are not stored
+    }
     int32_t m[2] = {INT_MIN, INT_MIN};
     const int run = min(n, w.nb - w.blk);  // blocks of this unit
     n -= run;
-    // one more turn than blocks: each reads a tile, then works on the one read before it
+    const int s0 = w.blk * kSub, s1 = (w.blk + run) * kSub;
 #pragma unroll 1
-    for (int i = fresh ? 1 : 0; i <= run; ++i) {
-      int32_t d[kSub][kCh][4];
-      if (i > 0) {
-#pragma unroll
-        for (int s = 0; s < kSub; ++s)
-#pragma unroll
-          for (int c = 0; c < kCh; ++c) {
-            d[s][c][0] = d[s][c][1] = d[s][c][2] = d[s][c][3] = 0;
-            mma16832(d[s][c], k_u8, k[s][0][c].x, k[s][1][c].x, k[s][0][c].y, k[s][1][c].y, q[c].x, q[c].y);
-            mma16832(d[s][c], k_u8, k[s][0][c].z, k[s][1][c].z, k[s][0][c].w, k[s][1][c].w, q[c].z, q[c].w);
-          }
+    for (int s = s0; s < s1; ++s) {
+      if (!fresh) {
+        if ((tile = ring.wait()) == 0) return false;
+        read(0);
+        fresh = true;
       }
-      if (i < run || n > 0) {
-        const uint32_t tile = ring.wait();
-        if (tile == 0) return false;
+      int32_t d[2][4];  // two chains of products
 #pragma unroll
-        for (int s = 0; s < kSub; ++s)
+      for (int c = 0; c < 2; ++c) d[c][0] = d[c][1] = d[c][2] = d[c][3] = 0;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int c = 0; c < kCh; ++c) {
-              const int row = 16 * s + 8 * e + n8;  // the TMA's swizzle on the 16-byte piece
-              const int piece = D == 128 ? ((t + 4 * c) ^ (row & 7)) : (t ^ ((row >> 1) & 3));
-              k[s][e][c] = lds_u128(tile + row * D + 16 * piece);
-            }
+      for (int c = 0; c < kK; ++c)
+        mma16832(d[c & 1], k_u8, k[c][0], k[c][1], k[c][2], k[c][3], q[c][0], q[c][1]);
+      // the next fragments, before the scores are stored
+      const int in = (s + 1) % kSub;
+      if (in != 0) {
+        read(in);
+      } else {
         __syncwarp();  // every lane has read the tile
         if (left > 0) issue();
+        fresh = false;
+        if (s + 1 < s1) {
+          if ((tile = ring.wait()) == 0) return false;
+          read(0);
+          fresh = true;
+        }
       }
-      if (i == 0) continue;
       // d[..][0], [1]: key n8, rows 2t and 2t + 1; [2], [3]: key n8 + 8
-      const int j0 = (w.blk + i - 1) * kKeys;
 #pragma unroll
-      for (int s = 0; s < kSub; ++s)
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            int32_t v = d[s][0][2 * e + r];
-            if (kCh == 2) v += d[s][kCh - 1][2 * e + r];
-            if (j0 + 16 * s + 8 * e + n8 >= x.len) v = INT_MIN;
-            // key n8 + 8 is kept two positions after key n8 (score_at)
-            if (2 * t + r < x.rows) sp[static_cast<size_t>(r) * a.ld_s + j0 + 16 * s + 2 * e] = v;
-            m[r] = imax(m[r], v);
-          }
+        for (int r = 0; r < 2; ++r) {
+          const int32_t v = 16 * s + 8 * e + n8 < x.len ? d[0][2 * e + r] + d[1][2 * e + r] : INT_MIN;
+          if (2 * t + r < x.rows) sp[static_cast<size_t>(r) * a.ld_s + 16 * s + 8 * e] = v;
+          m[r] = imax(m[r], v);
+        }
     }
-    fresh = true;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       m[0] = imax(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
@@ -540,108 +533,94 @@ __device__ __forceinline__ int own_pv_start(const SharedArgs& a, OwnRing& ring, 
 }
 
 // ---- phase C of the own rows: P.V of the same blocks ----
-// A = V^T: the thread (n8, t) reads D / 8 channels (from D / 8 n8) of the four
-// keys key_of(t, i), which make a fragment word per channel.  B = P: query row
-// n8, the same keys.  P of the next block is made while this one's V is read.
+// A = V^T: sixteen channels by 32 keys per product, transposed on the way from
+// shared memory; B = P: query row n8, keys 4 t .. + 3 and 16 + 4 t .. + 3.  P of the
+// next 32 keys is made while this one's V is read.
 template <int D>
 __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& ring, const HeadParamsDev* hp_s,
                                        const uint32_t* lut_s, Walk w, Walk ld, int left, int n) {
   constexpr int kKeys = kOwnBytes / D;
-  constexpr int kSub = kKeys / 16;
-  constexpr int kWords = D / 32;  // 4-channel words of a row per thread
+  constexpr int kStep = kKeys / 32;  // 32-key steps per block
+  constexpr int kM = D / 16;         // products per step
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
   while (n > 0) {
     Unit x;
     x.set(a, w);
     const int mine = min(n8, x.rows - 1);
     const uint32_t* ip = a.index + static_cast<size_t>(x.row + mine) * (a.ld_s / 4) + t;
-    uint32_t ix[kSub], p[kSub];  // index words of the block after next, P of the next
-    auto load_index = [&](int blk) {
-#pragma unroll
-      for (int s = 0; s < kSub; ++s)
-        ix[s] = 16 * (blk * kSub + s) < x.len ? ip[4 * (blk * kSub + s)] : 0x1F1F1F1Fu;
-    };
-    load_index(w.blk);
+    auto index_word = [&](int s) { return 16 * s < x.len ? ip[4 * s] : 0x1F1F1F1Fu; };  // of 16-key step s
+    const int run = min(n, w.nb - w.blk);  // blocks of this unit
+    n -= run;
+    const int s0 = w.blk * kStep, s1 = (w.blk + run) * kStep;
+    // of the next 32 keys and the 32 after them
+    uint32_t ix0 = index_word(2 * s0), ix1 = index_word(2 * s0 + 1);
+    uint32_t iy0 = index_word(2 * s0 + 2), iy1 = index_word(2 * s0 + 3);
     const uint32_t R = static_cast<uint32_t>(exact_R(__ldcg(a.row_z + x.at + mine)));  // < 2^25: Z >= 2^15
     const uint32_t lut = smem_u32(lut_s) + 128 * hp_s[a.per_head ? x.head + mine : 0].lut;
     uint32_t psum = 0;
-    int32_t o[D / 16][4];
+    int32_t o[kM][4];
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c)
+    for (int c = 0; c < kM; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[c][i] = 0;
-    const int run = min(n, w.nb - w.blk);  // blocks of this unit
-    n -= run;
-    // one more turn than blocks: each makes the P of its block, after the V work on the one before
+    // P of four keys (0 for rows the unit does not have)
+    auto make_p = [&](uint32_t word) {
+      uint32_t b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        b[e] = static_cast<uint32_t>(
+            (static_cast<unsigned long long>(lds_u32(lut + 4 * ((word >> (8 * e)) & 255u))) * R + (1ull << 31)) >> 32);
+      const uint32_t p = n8 < x.rows ? prefill::pack4(b[0], b[1], b[2], b[3]) : 0u;
+      psum = __dp4a(p, 0x01010101u, psum);
+      return p;
+    };
+    uint32_t p0 = make_p(ix0), p1 = make_p(ix1), tile = 0;
 #pragma unroll 1
-    for (int i = 0; i <= run; ++i) {
-      if (i > 0) {
-        const uint32_t tile = ring.wait();
-        if (tile == 0) return false;
+    for (int s = s0; s < s1; ++s) {
+      ix0 = iy0;
+      ix1 = iy1;
+      iy0 = index_word(2 * s + 4);
+      iy1 = index_word(2 * s + 5);
+      const int in = s % kStep;
+      if (in == 0 && (tile = ring.wait()) == 0) return false;
+      uint32_t n0 = 0, n1 = 0;
 #pragma unroll
-        for (int s = 0; s < kSub; ++s) {
-          uint32_t v[4][kWords];
+      for (int h = 0; h < 2; ++h) {  // half of the channels at a time
+        uint32_t v[kM / 2][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = 16 * s + key_of<D>(t, e);  // the TMA's swizzle on the 16-byte piece
-            if constexpr (D == 128) {
-              const uint4 y = lds_u128(tile + row * 128 + 16 * (n8 ^ (row & 7)));
-              v[e][0] = y.x;
-              v[e][1] = y.y;
-              v[e][2] = y.z;
-              v[e][3] = y.w;
-            } else {
-              const uint2 y = lds_u64(tile + row * 64 + 16 * ((n8 >> 1) ^ ((row >> 1) & 3)) + 8 * (n8 & 1));
-              v[e][0] = y.x;
-              v[e][1] = y.y;
-            }
-          }
-          if (s == kSub - 1) {
-            __syncwarp();  // every lane has read the tile
-            if (left > 0) {
-              ring.issue(&a.tm_vc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk);
-              if (--left > 0) ld.next(a, kKeys);
-            }
-          }
-          // bytes (key, channel c) -> word c holds four keys of channel c
-#pragma unroll
-          for (int q = 0; q < kWords; ++q) {
-            const uint32_t ab_lo = __byte_perm(v[0][q], v[1][q], 0x5140), ab_hi = __byte_perm(v[0][q], v[1][q], 0x7362);
-            const uint32_t cd_lo = __byte_perm(v[2][q], v[3][q], 0x5140), cd_hi = __byte_perm(v[2][q], v[3][q], 0x7362);
-            mma16816(o[2 * q], v_u8, __byte_perm(ab_lo, cd_lo, 0x5410), __byte_perm(ab_lo, cd_lo, 0x7632), p[s]);
-            mma16816(o[2 * q + 1], v_u8, __byte_perm(ab_hi, cd_hi, 0x5410), __byte_perm(ab_hi, cd_hi, 0x7632), p[s]);
+        for (int c = 0; c < kM / 2; ++c) ldmatrix2_trans(v[c], tile_at<D>(tile, 32 * in + lane, h * (kM / 2) + c));
+        if (h == 0) n0 = make_p(ix0);
+        else n1 = make_p(ix1);
+        if (h == 1 && in == kStep - 1) {
+          __syncwarp();  // every lane has read the tile
+          if (left > 0) {
+            ring.issue(&a.tm_vc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk);
+            if (--left > 0) ld.next(a, kKeys);
           }
         }
-      }
-      if (i < run) {
-        // P (0 for rows the unit does not have)
 #pragma unroll
-        for (int s = 0; s < kSub; ++s) {
-          uint32_t b[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            b[e] = static_cast<uint32_t>(
-                (static_cast<unsigned long long>(lds_u32(lut + 4 * ((ix[s] >> (8 * e)) & 255u))) * R + (1ull << 31)) >> 32);
-          p[s] = n8 < x.rows ? prefill::pack4(b[0], b[1], b[2], b[3]) : 0u;
-          psum = __dp4a(p[s], 0x01010101u, psum);
-        }
-        load_index(w.blk + i + 1);
+        for (int c = 0; c < kM / 2; ++c)
+          mma16832_pv(o[h * (kM / 2) + c], v_u8, v[c][0], v[c][1], v[c][2], v[c][3], p0, p1);
       }
+      // P past the run belongs to no step of this unit here: not counted below
+      if (s + 1 == s1) psum -= __dp4a(n0, 0x01010101u, __dp4a(n1, 0x01010101u, 0u));
+      p0 = n0;
+      p1 = n1;
     }
     if (v_u8) {
       psum += __shfl_xor_sync(0xffffffffu, psum, 1);
       psum += __shfl_xor_sync(0xffffffffu, psum, 2);
       if (t == 0 && n8 < x.rows) atomicAdd(a.row_p + x.at + n8, static_cast<int32_t>(psum));
     }
-    // o[c][0..1]: channel D/8 n8 + 2c, rows 2t, 2t + 1; o[c][2..3]: channel D/8 n8 + 2c + 1
+    // o[c][0], [1]: channel 16 c + n8, rows 2t and 2t + 1; [2], [3]: channel 16 c + 8 + n8
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       if (2 * t + r < x.rows) {
-        float* dst = a.acc + static_cast<size_t>(x.at + 2 * t + r) * D + D / 8 * n8;
+        float* dst = a.acc + static_cast<size_t>(x.at + 2 * t + r) * D + n8;
 #pragma unroll
-        for (int c = 0; c < D / 16; c += 2)
-          red_add4(dst + 2 * c, static_cast<float>(o[c][r]), static_cast<float>(o[c][2 + r]),
-                   static_cast<float>(o[c + 1][r]), static_cast<float>(o[c + 1][2 + r]));
+        for (int c = 0; c < kM; ++c)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) atomicAdd(dst + 16 * c + 8 * e, static_cast<float>(o[c][2 * e + r]));
       }
     if (n > 0) {
       w.blk += run - 1;
