@@ -49,14 +49,9 @@ class IntAttnError(RuntimeError):
 
 
 class _Scales(ctypes.Structure):
-    _fields_ = [("per_head", ctypes.c_int32),
-                ("s_q", ctypes.POINTER(ctypes.c_float)),
-                ("s_k", ctypes.POINTER(ctypes.c_float)),
-                ("s_v", ctypes.POINTER(ctypes.c_float)),
-                ("s_o", ctypes.POINTER(ctypes.c_float)),
-                ("clip_c", ctypes.POINTER(ctypes.c_float)),
-                ("z_k", ctypes.POINTER(ctypes.c_int32)),
-                ("z_v", ctypes.POINTER(ctypes.c_int32))]
+    # host arrays: float s_q, s_k, s_v, s_o, clip_c; int32 z_k, z_v
+    _fields_ = [("per_head", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in
+                                                 ("s_q", "s_k", "s_v", "s_o", "clip_c", "z_k", "z_v")]
 
 
 class _HeadParams(ctypes.Structure):
@@ -78,6 +73,15 @@ class _RopeNorm(ctypes.Structure):
 FloatArg = Union[float, Sequence[float], np.ndarray]
 
 
+def _host_array(x, dtype) -> np.ndarray:
+    """x as a contiguous 1-D host array (x itself where it is one)."""
+    if type(x) is np.ndarray and x.dtype == dtype and x.ndim == 1 and x.flags.c_contiguous:
+        return x
+    if type(x) is float or type(x) is int:
+        return np.array((x,), dtype)
+    return np.ascontiguousarray(np.atleast_1d(np.asarray(x)).astype(dtype, copy=False))
+
+
 @dataclasses.dataclass
 class Scales:
     """Quantisation scales (real = scale * code).  per_head: arrays of H.
@@ -95,24 +99,17 @@ class Scales:
     z_v: Optional[FloatArg] = None
 
     def _c(self):
-        arrs = [np.ascontiguousarray(np.atleast_1d(np.asarray(x, dtype=np.float32)))
-                for x in (self.s_q, self.s_k, self.s_v, self.s_o)]
-        fp = ctypes.POINTER(ctypes.c_float)
-        clip = None
+        f32 = np.float32
+        arrs = [_host_array(self.s_q, f32), _host_array(self.s_k, f32), _host_array(self.s_v, f32),
+                _host_array(self.s_o, f32)]
+        s = _Scales(int(bool(self.per_head)), *[a.__array_interface__["data"][0] for a in arrs])
         if self.clip is not None:
-            clip = np.ascontiguousarray(np.atleast_1d(np.asarray(self.clip, dtype=np.float32)))
-            arrs.append(clip)
-        ip = ctypes.POINTER(ctypes.c_int32)
-        zs = []
-        for z in (self.z_k, self.z_v):
-            if z is None:
-                zs.append(ip())
-            else:
-                za = np.ascontiguousarray(np.atleast_1d(np.asarray(z)).astype(np.int32))
-                arrs.append(za)
-                zs.append(za.ctypes.data_as(ip))
-        s = _Scales(int(bool(self.per_head)), *[a.ctypes.data_as(fp) for a in arrs[:4]],
-                    clip.ctypes.data_as(fp) if clip is not None else fp(), *zs)
+            arrs.append(_host_array(self.clip, f32))
+            s.clip_c = arrs[-1].__array_interface__["data"][0]
+        for name, z in (("z_k", self.z_k), ("z_v", self.z_v)):
+            if z is not None:
+                arrs.append(_host_array(z, np.int32))
+                setattr(s, name, arrs[-1].__array_interface__["data"][0])
         return s, arrs  # keep the arrays alive for the duration of the call
 
 
@@ -501,34 +498,47 @@ def quantize_zp(x, per_head: bool, out=None, scales=None, zero_points=None, stre
 # ------------------------------------------------ rows, caches and their decode
 
 class _On:
-    """Makes `device` and `stream` (None: the device's current stream) current
-    for a call, so that what the call allocates belongs to the stream it runs
-    on; gives the stream's handle."""
+    """Makes `device` and `stream` current for a call, so that what the call
+    allocates belongs to the stream it runs on; gives the stream's handle."""
 
     def __init__(self, device, stream):
-        import torch
-        self.guards = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        self.device, self.stream = device, stream
+        self.device, self.stream, self.guards = device, stream, []
 
     def __enter__(self) -> int:
         import torch
-        for g in self.guards:
-            g.__enter__()
+        self.guards.append(torch.cuda.device(self.device))
+        self.guards[0].__enter__()
         s = self.stream
-        if s is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        if not hasattr(s, "cuda_stream"):
-            s = torch.cuda.ExternalStream(int(s), device=self.device)
-        g = torch.cuda.stream(s)
-        g.__enter__()
-        self.guards.append(g)
-        return s.cuda_stream
+        if s is not None:
+            if not hasattr(s, "cuda_stream"):
+                s = torch.cuda.ExternalStream(int(s), device=self.device)
+            self.guards.append(torch.cuda.stream(s))
+            self.guards[1].__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
+
+
+class _Here:
+    """_On for the current device and its current stream: nothing to switch."""
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self) -> int:
+        return self.handle
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _on(device, stream):
+    import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(torch._C._cuda_getCurrentRawStream(device.index))
+    return _On(device, stream)
 
 
 def _check_entries(scales: Scales, n_q: int, n_kv: int, names):
@@ -539,23 +549,37 @@ def _check_entries(scales: Scales, n_q: int, n_kv: int, names):
         if x is None:
             continue
         want = (n_q if name in ("s_q", "s_o", "clip") else n_kv) if scales.per_head else 1
-        if np.size(x) < want:
-            raise ValueError(f"scales.{name} holds {np.size(x)} entries; {want} are needed")
+        n = x.size if type(x) is np.ndarray else np.size(x)
+        if n < want:
+            raise ValueError(f"scales.{name} holds {n} entries; {want} are needed")
 
 
-def _rows(t, name: str, device, dtype, heads=None) -> _Rows:
+def _rows(t, name: str, device, dtype) -> _Rows:
     """A [B, heads, L, d] fp16 / bf16 CUDA tensor whose channels are contiguous."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in (torch.float16, torch.bfloat16):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _row_types():
         raise TypeError(f"{name} must be a CUDA float16 or bfloat16 tensor")
-    if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
-        raise ValueError(f"{name} must be [B, heads, L, d] with contiguous channels")
-    if t.device != device or t.dtype != dtype:
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, heads, L, d]")
+    B, h, L, d = t.shape
+    sb, sh, sl, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    if t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be on {device} in {dtype}")
-    sb, sh, sl, _ = t.stride()
-    B, h, L, _ = t.shape
     # the stride of an extent of one is never used
     return _Rows(t.data_ptr(), sb if B > 1 else 0, sh if h > 1 else 0, sl if L > 1 else 0)
+
+
+_ROW_TYPES = {}
+
+
+def _row_types():
+    """torch type -> INTATTN_DTYPE_*, of the row operators' floating tensors."""
+    if not _ROW_TYPES:
+        import torch
+        _ROW_TYPES.update({torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16})
+    return _ROW_TYPES
 
 
 def _index_tensor(t, name: str, shape, device):
@@ -633,7 +657,7 @@ def qk_norm_rope(q, k, norm: RopeNorm, q_out=None, k_out=None, stream=None):
     elif k_out is not None:
         raise ValueError("k_out without k")
     c = norm._c(B, L, d, dev)
-    with _On(dev, stream) as st:
+    with _on(dev, stream) as st:
         if q_out is None:
             q_out = torch.empty((B, H, L, d), dtype=dt, device=dev)
         if k is not None and k_out is None:
@@ -643,20 +667,18 @@ def qk_norm_rope(q, k, norm: RopeNorm, q_out=None, k_out=None, stream=None):
             kor = _rows(k_out, "k_out", dev, dt)
         if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
             raise ValueError("outputs must match q and k")
-        _check(lib().intattn_qk_norm_rope(qr, kr, c, DTYPE_BF16 if dt == torch.bfloat16 else DTYPE_FP16, B, H, Hkv, L,
-                                          d, qor, kor, st), "intattn_qk_norm_rope")
+        _check(lib().intattn_qk_norm_rope(qr, kr, c, _row_types()[dt], B, H, Hkv, L, d, qor, kor, st), "intattn_qk_norm_rope")
     return q_out, k_out
 
 
-def _check_cache(t, name: str, zero_point, bits: int, B: int, Hkv: int, d: int, device):
+def _check_cache(t, name: str, zero_point, bits: int, shape, device):
+    """A cache of `shape` [B, Hkv, Lmax, bytes of a row]."""
     import torch
-    if bits not in (8, 4):
-        raise ValueError("bits must be 8 or 4")
     want = torch.uint8 if bits == 4 or zero_point is not None else torch.int8
     if not isinstance(t, torch.Tensor) or t.dtype != want or t.device != device:
         raise TypeError(f"{name} must be a {want} tensor on {device}")
-    if t.dim() != 4 or t.shape[:2] != (B, Hkv) or t.shape[3] != d * bits // 8 or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [{B}, {Hkv}, Lmax, {d * bits // 8}]")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}")
 
 
 def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bits: int = 8, q=None, q_out=None,
@@ -675,11 +697,14 @@ def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bit
     B, Hkv, L, d = k.shape
     if v.shape != k.shape:
         raise ValueError("v must match k")
-    _check_cache(k_cache, "k_cache", scales.z_k, bits, B, Hkv, d, dev)
-    _check_cache(v_cache, "v_cache", scales.z_v, bits, B, Hkv, d, dev)
+    if bits not in (8, 4):
+        raise ValueError("bits must be 8 or 4")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise TypeError("k_cache must be a [B, Hkv, Lmax, d] tensor")
     Lmax = k_cache.shape[2]
-    if v_cache.shape[2] != Lmax:
-        raise ValueError("the caches must have one capacity")
+    shape = (B, Hkv, Lmax, d * bits // 8)
+    _check_cache(k_cache, "k_cache", scales.z_k, bits, shape, dev)
+    _check_cache(v_cache, "v_cache", scales.z_v, bits, shape, dev)
     H, qr = 0, None
     if q is not None:
         qr = _rows(q, "q", dev, dt)
@@ -693,14 +718,14 @@ def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bit
     lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
     c = None if norm is None else norm._c(B, L, d, dev)
     sc, keep = scales._c()
-    with _On(dev, stream) as st:
+    with _on(dev, stream) as st:
         if q is not None:
             if q_out is None:
                 q_out = torch.empty((B, H, L, d), dtype=torch.int8, device=dev)
             _check_tensor(q_out, "q_out")
             if q_out.shape != q.shape or q_out.device != dev:
                 raise ValueError("q_out must match q")
-        rc = lib().intattn_cache_write(kr, vr, qr, DTYPE_BF16 if dt == torch.bfloat16 else DTYPE_FP16, sc, int(bits), c,
+        rc = lib().intattn_cache_write(kr, vr, qr, _row_types()[dt], sc, int(bits), c,
                                        B, H, Hkv, L, Lmax, d, sp, lp, k_cache.data_ptr(), v_cache.data_ptr(),
                                        None if q is None else q_out.data_ptr(), st)
     del keep
@@ -719,26 +744,25 @@ def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bi
     if bits not in (8, 4):
         raise ValueError("bits must be 8 or 4")
     dev = k_cache.device
-    B, Hkv, Lmax, d = k_cache.shape
+    shape = k_cache.shape
+    B, Hkv, Lmax, d = shape
     d = d * 8 // bits
     L = int(L)
     if L < 0:
         raise ValueError("L must not be negative")
-    _check_cache(k_cache, "k_cache", scales.z_k, bits, B, Hkv, d, dev)
+    _check_cache(k_cache, "k_cache", scales.z_k, bits, shape, dev)
     if v_cache is not None:
-        _check_cache(v_cache, "v_cache", scales.z_v, bits, B, Hkv, d, dev)
-        if v_cache.shape != k_cache.shape:
-            raise ValueError("the caches must match")
+        _check_cache(v_cache, "v_cache", scales.z_v, bits, shape, dev)
     elif v_out is not None:
         raise ValueError("v_out without v_cache")
     dt = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
-    if dt not in (torch.float16, torch.bfloat16):
+    if dt not in _row_types():
         raise TypeError("dtype must be float16 or bfloat16")
     _check_entries(scales, 0, Hkv, ("s_k", "z_k") + (("s_v", "z_v") if v_cache is not None else ()))
     sp = _index_tensor(start, "start", (B,), dev)
     lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
     sc, keep = scales._c()
-    with _On(dev, stream) as st:
+    with _on(dev, stream) as st:
         if k_out is None:
             k_out = torch.empty((B, Hkv, L, d), dtype=dt, device=dev)
         if v_out is None and v_cache is not None:
@@ -751,7 +775,7 @@ def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bi
             if t.shape != (B, Hkv, L, d) or not t.is_contiguous():
                 raise ValueError(f"{n} must be contiguous {[B, Hkv, L, d]}")
         rc = lib().intattn_cache_read(k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), sc, int(bits),
-                                      B, Hkv, L, Lmax, d, sp, lp, DTYPE_BF16 if dt == torch.bfloat16 else DTYPE_FP16,
+                                      B, Hkv, L, Lmax, d, sp, lp, _row_types()[dt],
                                       k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), st)
     del keep
     _check(rc, "intattn_cache_read")
@@ -799,7 +823,7 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lengths, scales: Scal
     if dt not in kinds:
         raise TypeError("dtype must be int8, float16 or bfloat16")
     sc, keep = scales._c()
-    with _On(dev, stream) as st:
+    with _on(dev, stream) as st:
         if out is None:
             out = torch.empty((B, H, 1, d), dtype=dt, device=dev)
         if not isinstance(out, torch.Tensor) or out.dtype != dt or out.device != dev:

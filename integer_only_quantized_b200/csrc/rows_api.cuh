@@ -46,25 +46,32 @@ void set_input(RowTensor* t, const intattn_rows_t* r, int heads) {
   t->heads = heads;
 }
 
-// Heads a warp takes of a token: as many as it holds in flight (D / 8 lanes
-// and four loads per lane) when that still gives every SM several warps,
-// else one step's worth, so that few tokens spread over more SMs.
+// A warp takes a batch of one tensor's heads of a token: as many as it holds in
+// flight (D / 8 lanes and four loads per lane) when that still gives every SM
+// several warps, else one load's worth, so that few tokens spread over more SMs.
 template <bool kCodes>
 int rows_launch(RowArgs& a, int d, cudaStream_t st) {
   int sms = 0;
   if (sm_count(&sms) != INTATTN_OK) return INTATTN_ERR_CUDA;
-  const int per_step = 256 / d, batch = 4 * per_step;
+  const int per_load = 256 / d;
   const long long tokens = static_cast<long long>(a.B) * a.L;
-  const bool many = tokens * ((a.heads + batch - 1) / batch) >= 8ll * sms;
-  a.heads_per_item = many ? batch : per_step;
-  a.items_per_token = (a.heads + a.heads_per_item - 1) / a.heads_per_item;
-  a.items = tokens * a.items_per_token;
-  const long long grid = (a.items + intattn::rows::kWarps - 1) / intattn::rows::kWarps;
-  if (grid > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
+  for (a.batch = 4 * per_load;; a.batch = per_load) {
+    a.warps_per_token = 0;
+    a.first[0] = a.first[1] = a.first[2] = INT32_MAX;  // tensors that are not there have no warps
+    for (int i = 0; i < a.n_tensors; ++i) {
+      a.first[i] = a.warps_per_token;
+      a.warps_per_token += (a.t[i].heads + a.batch - 1) / a.batch;
+    }
+    if (a.batch == per_load || tokens * a.warps_per_token >= 8ll * sms) break;
+  }
+  const long long warps = tokens * a.warps_per_token;
+  if (warps > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
+  a.warps = static_cast<uint32_t>(warps);
+  const unsigned grid = static_cast<unsigned>((warps + intattn::rows::kWarps - 1) / intattn::rows::kWarps);
   if (d == 64)
-    intattn::rows::rows_kernel<64, kCodes><<<static_cast<unsigned>(grid), intattn::rows::kThreads, 0, st>>>(a);
+    intattn::rows::rows_kernel<64, kCodes><<<grid, intattn::rows::kThreads, 0, st>>>(a);
   else
-    intattn::rows::rows_kernel<128, kCodes><<<static_cast<unsigned>(grid), intattn::rows::kThreads, 0, st>>>(a);
+    intattn::rows::rows_kernel<128, kCodes><<<grid, intattn::rows::kThreads, 0, st>>>(a);
   return note_launch(cudaGetLastError());
 }
 
@@ -115,7 +122,6 @@ int intattn_qk_norm_rope(const intattn_rows_t* q, const intattn_rows_t* k, const
     a.t[i].w = i ? rn->w_k : rn->w_q;
     a.t[i].rope = 1;
   }
-  a.heads = H + Hkv;
   a.B = B;
   a.L = L;
   a.bf16 = dtype == INTATTN_DTYPE_BF16 ? 1 : 0;
@@ -166,7 +172,6 @@ int intattn_cache_write(const intattn_rows_t* k, const intattn_rows_t* v, const 
     t.bits = i < 2 ? bits : 8;
     t.asym = i == 0 ? scales->z_k != nullptr : i == 1 ? scales->z_v != nullptr : 0;
     t.sc = i * S;
-    a.heads += heads;
   }
   a.B = B;
   a.L = L;
@@ -214,17 +219,17 @@ int intattn_cache_read(const void* k_cache, const void* v_cache, const intattn_s
   a.bits = bits;
   a.asym_k = scales->z_k ? 1 : 0;
   a.asym_v = scales->z_v ? 1 : 0;
-  a.rows = static_cast<int64_t>(B) * Hkv * L;
   a.start = start;
   a.lengths = lengths;
-  const long long threads = a.rows * a.n_tensors * (d / 16);
-  const long long grid = (threads + intattn::rows::kThreads - 1) / intattn::rows::kThreads;
+  const int per_cta = intattn::rows::kReadThreads / (d / 8) * intattn::rows::kReadUnroll;
+  a.chunks = (L + per_cta - 1) / per_cta;
+  const long long grid = static_cast<long long>(a.chunks) * B * Hkv * a.n_tensors;
   if (grid > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (d == 64)
-    intattn::rows::read_kernel<64><<<static_cast<unsigned>(grid), intattn::rows::kThreads, 0, st>>>(a);
+    intattn::rows::read_kernel<64><<<static_cast<unsigned>(grid), intattn::rows::kReadThreads, 0, st>>>(a);
   else
-    intattn::rows::read_kernel<128><<<static_cast<unsigned>(grid), intattn::rows::kThreads, 0, st>>>(a);
+    intattn::rows::read_kernel<128><<<static_cast<unsigned>(grid), intattn::rows::kReadThreads, 0, st>>>(a);
   return note_launch(cudaGetLastError());
 }
 

@@ -3,18 +3,21 @@
 // scales as they are written into a cache, and reading cache rows back.
 //
 // A row is one head of one token: d = 64 or 128 channels.  D / 8 lanes hold a
-// row, eight channels (one 16-byte load) each, and everything between the
-// load and the store stays in fp32 registers:
+// row, two groups of four channels each, and everything between the load
+// and the store stays in fp32 registers:
 //   norm      y = x / sqrt(mean x^2 + eps) * w, the sum over the row's lanes
 //             by shuffles
 //   rotation  pairs (a, b) of the first rot channels -> (a c - b s, a s + b c)
-//             with (c, s) from the caller's table at the token's position;
-//             half-split pairs (f, f + rot/2) sit rot/16 lanes apart (one
-//             shuffle per channel), interleaved pairs (2f, 2f + 1) in one lane
+//             with (c, s) from the caller's table at the token's position.  A
+//             lane's two groups are those that pair with each other (f and
+//             f + rot/2, or neighbours where pairs are interleaved), so the rotation
+//             needs no other lane: with eight consecutive channels per lane
+//             and a shuffle per channel the rows of a LLaMA-7B prefill took
+//             82 us instead of 63
 //   codes     clamp(rint(RN32(y inv)) + z), or one rounding to fp16 / bf16
-// All of it is bound by memory (2 bytes in, 2, 1 or 1/2 byte out per channel
-// for a handful of instructions), or, for the few rows of a decode step, by
-// the launch and one round trip.
+// All of it is bound by memory (2 bytes in, 2, 1 or 1/2 byte out per channel),
+// closely followed by the instructions in between; for the few rows of a
+// decode step by the launch and one round trip.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,11 +46,12 @@ struct RowTensor {
 
 struct RowArgs {
   RowTensor t[3];              // heads of tensor 0, then 1, then 2
-  int32_t n_tensors, heads;    // heads: over all tensors
+  int32_t n_tensors;
   int32_t B, L, Lmax, bf16, per_head;
-  int32_t heads_per_item;      // heads of one token that a warp handles
-  int32_t items_per_token;
-  int64_t items;               // B * L * items_per_token
+  int32_t batch;               // heads of one token and tensor that a warp handles
+  int32_t first[3];            // a token's warps: tensor x has first[x] .. first[x + 1] - 1
+  int32_t warps_per_token;
+  uint32_t warps;              // B * L * warps_per_token
   const int32_t* start;        // [B] first cache row, or null
   const int32_t* lengths;      // [B] rows of each sequence, or null: all L
   const int32_t* positions;    // [B, L], or null: no rotation
@@ -62,7 +66,7 @@ struct ReadArgs {
   const uint8_t* in[2];   // caches [B, H, Lmax, d] (4 bits: d / 2 bytes a row)
   void* out[2];           // [B, H, L, d] fp16 / bf16
   int32_t n_tensors, B, H, L, Lmax, bf16, per_head, bits, asym_k, asym_v;
-  int64_t rows;           // per tensor: B * H * L
+  int32_t chunks;         // CTAs per (b, h): each takes kRows rows
   const int32_t* start;
   const int32_t* lengths;
   float scale[2 * INTATTN_MAX_HEADS];
@@ -74,12 +78,40 @@ namespace rows {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
-// rint(RN32(y inv)) as an integer in [-2^21, 2^21]: infinities and values
-// beyond the range saturate there (every code range lies inside), NaN gives 0.
-__device__ __forceinline__ int32_t code_of(float y, float inv) {
-  const float p = __fmul_rn(y, inv);
-  const float q = fminf(fmaxf(p, -2097152.0f), 2097152.0f);  // NaN: -2097152
-  return p == p ? __float2int_rn(q) : 0;
+// rint(RN32(y inv)) of four values, clamped to [lo, hi], plus z, in the low
+// byte of each word.  Adding 1.5 * 2^23 rounds to an integer with ties to even
+// and leaves it in the sum's low bits; infinities and values past the range end at
+// lo or hi, NaN gives z.
+__device__ __forceinline__ void codes4(const float (&y)[4], float inv, float lo, float hi, int32_t z, uint32_t (&c)[4]) {
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float p = __fmul_rn(y[i], inv);
+    nan |= !(p == p);
+    c[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(p, lo), hi), 12582912.0f)) + static_cast<uint32_t>(z);
+  }
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = __fmul_rn(y[i], inv);
+      if (!(p == p)) c[i] = static_cast<uint32_t>(z);
+    }
+  }
+}
+
+__device__ __forceinline__ void to_float4(uint2 v, bool bf16, float (&f)[4]) {
+  const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (bf16) {
+      f[2 * i] = __uint_as_float(w[i] << 16);  // bf16 = high half of an fp32
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b, bool bf16) {
@@ -95,33 +127,55 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b, bool bf16) {
 template <int D, bool kCodes>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a) {
   constexpr int kLpr = D / 8;           // lanes per row
-  constexpr int kRpw = 32 / kLpr;       // rows (heads) per warp and step
-  constexpr int kUnroll = 4;            // steps whose loads are in flight together
+  constexpr int kRpw = 32 / kLpr;       // rows (heads) per warp and load
+  constexpr int kUnroll = 4;            // loads in flight per lane
   const int lane = threadIdx.x & 31;
-  const int piece = lane % kLpr;        // channels 8 piece .. 8 piece + 7
+  const int piece = lane % kLpr;
   const int sub = lane / kLpr;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (item >= a.items) return;
-  const int64_t token = item / a.items_per_token;
-  const int h0 = static_cast<int>(item - token * a.items_per_token) * a.heads_per_item;
-  const int h1 = min(a.heads, h0 + a.heads_per_item);
-  const int b = static_cast<int>(token / a.L);
-  const int t = static_cast<int>(token - static_cast<int64_t>(b) * a.L);
+  const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (id >= a.warps) return;
+  const uint32_t token = id / static_cast<uint32_t>(a.warps_per_token);
+  const int k = static_cast<int>(id - token * a.warps_per_token);
+  const int x = k >= a.first[2] ? 2 : k >= a.first[1] ? 1 : 0;
+  const RowTensor& rt = a.t[x];
+  const int h0 = (k - a.first[x]) * a.batch;
+  const int h1 = min(rt.heads, h0 + a.batch);
+  const int b = static_cast<int>(token / static_cast<uint32_t>(a.L));
+  const int t = static_cast<int>(token) - b * a.L;
+
+  // The lane's groups: channels g0 .. g0 + 3 and g1 .. g1 + 3.
+  const bool rope = a.positions != nullptr && rt.rope;  // uniform over the warp
+  const bool split = rope && !a.interleaved;
+  const bool turn = rope && 8 * piece < a.rot;
+  const int g0 = split && turn ? 4 * piece : 8 * piece;
+  const int g1 = split && turn ? 4 * piece + a.rot / 2 : 8 * piece + 4;
+
+  // the rows first: nothing below is needed for them
+  const uint16_t* in = static_cast<const uint16_t*>(rt.in) + b * rt.isb + t * rt.isl;
+  uint2 raw[kUnroll][2];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int h = h0 + u * kRpw + sub;
+    raw[u][0] = raw[u][1] = make_uint2(0, 0);
+    if (h < h1) {
+      raw[u][0] = *reinterpret_cast<const uint2*>(in + h * rt.ish + g0);
+      raw[u][1] = *reinterpret_cast<const uint2*>(in + h * rt.ish + g1);
+    }
+  }
 
   if (a.lengths != nullptr && t >= a.lengths[b]) return;  // a padded row
-  int slot = t;
+  int row = t;
   if (a.start != nullptr) {
-    const int64_t row = static_cast<int64_t>(a.start[b]) + t;
-    if (row < 0 || row >= a.Lmax) {
+    const int64_t slot = static_cast<int64_t>(a.start[b]) + t;
+    if (slot < 0 || slot >= a.Lmax) {
       if (lane == 0) atomicOr(&g_device_error, kErrParamRange);
       return;
     }
-    slot = static_cast<int>(row);
+    if (rt.cache) row = static_cast<int>(slot);
   }
-
-  // cos and sin of this lane's channels (kept for every head of the token)
-  float cs[8], sn[8];
-  bool turn = false;
+  // cos and sin of the lane's four pairs: split, pair i is channels g0 + i and
+  // g1 + i; interleaved, pairs 0 and 1 lie in the first group, 2 and 3 in the second
+  float4 cs[2] = {};
   if (a.positions != nullptr) {
     const int pos = a.positions[token];
     if (pos < 0) return;  // a padded row
@@ -129,193 +183,147 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       if (lane == 0) atomicOr(&g_device_error, kErrParamRange);
       return;
     }
-    turn = 8 * piece < a.rot;
     if (turn) {
-      const int half = a.rot / 2;
-      const float2* row = a.table + static_cast<int64_t>(pos) * half;
-      if (a.interleaved) {
-        const float4* p = reinterpret_cast<const float4*>(row + 4 * piece);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 v = __ldg(p + i);
-          cs[4 * i] = cs[4 * i + 1] = v.x;
-          sn[4 * i] = -v.y;  // the pair's first: a c - b s
-          sn[4 * i + 1] = v.y;
-          cs[4 * i + 2] = cs[4 * i + 3] = v.z;
-          sn[4 * i + 2] = -v.w;
-          sn[4 * i + 3] = v.w;
-        }
-      } else {
-        const bool first = 8 * piece < half;
-        const float4* p = reinterpret_cast<const float4*>(row + (first ? 8 * piece : 8 * piece - half));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 v = __ldg(p + i);
-          cs[2 * i] = v.x;
-          sn[2 * i] = first ? -v.y : v.y;
-          cs[2 * i + 1] = v.z;
-          sn[2 * i + 1] = first ? -v.w : v.w;
-        }
-      }
+      const float4* p = reinterpret_cast<const float4*>(a.table + static_cast<int64_t>(pos) * (a.rot / 2) + 4 * piece);
+      cs[0] = __ldg(p);
+      cs[1] = __ldg(p + 1);
     }
   }
-  // the lane that holds the other half of this lane's pairs (half-split)
-  const int hop = a.rot / 16;
-  const int partner = !turn ? lane : (8 * piece < a.rot / 2 ? lane + hop : lane - hop);
-
-  // tensor of head g of the token, and the head within it
-  auto locate = [&](int g, int& x, int& h) {
-    x = 0;
-    h = g;
-    if (h >= a.t[0].heads) {
-      h -= a.t[0].heads;
-      x = 1;
-      if (a.n_tensors > 2 && h >= a.t[1].heads) {
-        h -= a.t[1].heads;
-        x = 2;
-      }
-    }
-  };
-
-  for (int base = h0; base < h1; base += kRpw * kUnroll) {
-    uint4 raw[kUnroll];
+  float4 w[2] = {};
+  if (rt.w != nullptr) {
+    w[0] = __ldg(reinterpret_cast<const float4*>(rt.w + g0));
+    w[1] = __ldg(reinterpret_cast<const float4*>(rt.w + g1));
+  }
+  uint8_t* out8 = static_cast<uint8_t*>(rt.out);
+  const int64_t base = b * rt.osb + static_cast<int64_t>(row) * rt.osl;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int g = base + u * kRpw + sub;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (g < h1) {
-        int x, h;
-        locate(g, x, h);
-        const RowTensor& rt = a.t[x];
-        raw[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(rt.in) + b * rt.isb + h * rt.ish +
-                                                 t * rt.isl + 8 * piece);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int g = base + u * kRpw + sub;
-      if (base + u * kRpw >= h1) break;  // uniform over the warp
-      const bool mine = g < h1;
-      int x, h;
-      locate(mine ? g : h1 - 1, x, h);
-      const RowTensor& rt = a.t[x];
-      float y[8];
-      quant::to_float8(raw[u], a.bf16, y);
-      // norm (the shuffles run on every lane: rows of a warp may differ in kind)
+  for (int u = 0; u < kUnroll; ++u) {
+    if (h0 + u * kRpw >= h1) break;  // uniform over the warp
+    const int h = h0 + u * kRpw + sub;
+    float y[2][4];
+    to_float4(raw[u][0], a.bf16, y[0]);
+    to_float4(raw[u][1], a.bf16, y[1]);
+    if (rt.w != nullptr) {
       float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+      for (int i = 0; i < 4; ++i) ss = fmaf(y[1][i], y[1][i], fmaf(y[0][i], y[0][i], ss));
 #pragma unroll
       for (int o = kLpr / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (rt.w != nullptr) {
-        const float r = __fdiv_rn(1.0f, __fsqrt_rn(ss * (1.0f / D) + a.eps));
-        const float4* wp = reinterpret_cast<const float4*>(rt.w + 8 * piece);
-        const float4 w0 = __ldg(wp), w1 = __ldg(wp + 1);
-        const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      const float r = __frsqrt_rn(fmaf(ss, 1.0f / D, a.eps));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * r * wv[i];
+      for (int g = 0; g < 2; ++g) {
+        y[g][0] = y[g][0] * r * w[g].x;
+        y[g][1] = y[g][1] * r * w[g].y;
+        y[g][2] = y[g][2] * r * w[g].z;
+        y[g][3] = y[g][3] * r * w[g].w;
       }
-      if (a.positions != nullptr) {  // uniform over the warp
-        const bool rot = turn && rt.rope;
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          float o0, o1;
-          if (a.interleaved) {
-            o0 = y[i + 1];
-            o1 = y[i];
-          } else {
-            o0 = __shfl_sync(0xffffffffu, y[i], partner);
-            o1 = __shfl_sync(0xffffffffu, y[i + 1], partner);
-          }
-          if (rot) {
-            y[i] = fmaf(y[i], cs[i], o0 * sn[i]);
-            y[i + 1] = fmaf(y[i + 1], cs[i + 1], o1 * sn[i + 1]);
-          }
-        }
-      }
-      if (!mine) continue;
-      const int64_t at = b * rt.osb + h * rt.osh + static_cast<int64_t>(rt.cache ? slot : t) * rt.osl + 8 * piece;
-      if constexpr (!kCodes) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(rt.out) + at) =
-            make_uint4(pack_half2(y[0], y[1], a.bf16), pack_half2(y[2], y[3], a.bf16), pack_half2(y[4], y[5], a.bf16),
-                       pack_half2(y[6], y[7], a.bf16));
+    }
+    if (turn) {
+      auto rotate = [](float& p, float& q, float c, float s) {
+        const float x0 = p, x1 = q;
+        p = fmaf(x0, c, -(x1 * s));
+        q = fmaf(x1, c, x0 * s);
+      };
+      if (split) {
+        rotate(y[0][0], y[1][0], cs[0].x, cs[0].y);
+        rotate(y[0][1], y[1][1], cs[0].z, cs[0].w);
+        rotate(y[0][2], y[1][2], cs[1].x, cs[1].y);
+        rotate(y[0][3], y[1][3], cs[1].z, cs[1].w);
       } else {
-        const int e = rt.sc + (a.per_head ? h : 0);
-        const float inv = a.inv[e];
-        const int32_t z = rt.asym ? a.zero[e] : 0;
-        const int32_t hi = rt.asym ? (1 << rt.bits) - 1 : (1 << (rt.bits - 1)) - 1;
-        const int32_t lo = rt.asym ? 0 : -hi;
-        uint32_t c[8];
+        rotate(y[0][0], y[0][1], cs[0].x, cs[0].y);
+        rotate(y[0][2], y[0][3], cs[0].z, cs[0].w);
+        rotate(y[1][0], y[1][1], cs[1].x, cs[1].y);
+        rotate(y[1][2], y[1][3], cs[1].z, cs[1].w);
+      }
+    }
+    if (h >= h1) continue;
+    const int64_t at = base + h * rt.osh;
+    if constexpr (!kCodes) {
+      uint16_t* dst = static_cast<uint16_t*>(rt.out) + at;
+      *reinterpret_cast<uint2*>(dst + g0) = make_uint2(pack_half2(y[0][0], y[0][1], a.bf16), pack_half2(y[0][2], y[0][3], a.bf16));
+      *reinterpret_cast<uint2*>(dst + g1) = make_uint2(pack_half2(y[1][0], y[1][1], a.bf16), pack_half2(y[1][2], y[1][3], a.bf16));
+    } else {
+      const int e = rt.sc + (a.per_head ? h : 0);
+      const int32_t z = rt.asym ? a.zero[e] : 0;
+      const int32_t top = rt.asym ? (1 << rt.bits) - 1 : (1 << (rt.bits - 1)) - 1;
+      const float lo = static_cast<float>(rt.asym ? -z : -top), hi = static_cast<float>(top - z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = static_cast<uint32_t>(min(max(code_of(y[i], inv) + z, lo), hi));
+      for (int g = 0; g < 2; ++g) {
+        uint32_t c[4];
+        codes4(y[g], a.inv[e], lo, hi, z, c);
+        const int64_t to = at + (g ? g1 : g0);
         if (rt.bits == 8) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(rt.out) + at) =
-              make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
-                         __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
-        } else {
-          uint32_t w = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w |= (c[i] & 15u) << (4 * i);  // channel 2t in the low nibble of byte t
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(rt.out) + at / 2) = w;
+          *reinterpret_cast<uint32_t*>(out8 + to) =
+              __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        } else {  // channel 2t in the low nibble of byte t
+          *reinterpret_cast<uint16_t*>(out8 + to / 2) = static_cast<uint16_t>(
+              (c[0] & 15u) | ((c[1] & 15u) << 4) | ((c[2] & 15u) << 8) | ((c[3] & 15u) << 12));
         }
       }
     }
   }
 }
 
-// Values s (c - z) of cache rows.  Sixteen channels per thread: one 16-byte
-// load of int8 codes (8 bytes of int4 codes) and two 16-byte stores.
+// Values s (c - z) of cache rows.  A lane takes eight channels of a row (an 8-byte
+// load of int8 codes, 4 bytes of int4 codes; one 16-byte store, so that a warp's store is one
+// contiguous run), of kUnroll rows.
+constexpr int kReadThreads = 256;
+constexpr int kReadUnroll = 8;
 template <int D>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int kLpr = D / 16;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int piece = static_cast<int>(i % kLpr);
-  int64_t row = i / kLpr;  // over the tensors' rows
-  if (row >= a.rows * a.n_tensors) return;
-  const int x = row >= a.rows ? 1 : 0;
-  row -= x * a.rows;
-  const int64_t bh = row / a.L;
-  const int t = static_cast<int>(row - bh * a.L);
-  const int b = static_cast<int>(bh / a.H);
-  const int h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H);
-  if (a.lengths != nullptr && t >= a.lengths[b]) return;
-  const int64_t slot = static_cast<int64_t>(a.start[b]) + t;
-  if (slot < 0 || slot >= a.Lmax) {
-    if (piece == 0) atomicOr(&g_device_error, kErrParamRange);
-    return;
-  }
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int kLpr = D / 8;
+  constexpr int kStep = kReadThreads / kLpr;      // rows per load
+  constexpr int kRows = kStep * kReadUnroll;      // rows per CTA
+  const int piece = threadIdx.x % kLpr;
+  const uint32_t bhx = blockIdx.x / static_cast<uint32_t>(a.chunks);  // (tensor, b, h)
+  const int t0 = static_cast<int>(blockIdx.x - bhx * a.chunks) * kRows + threadIdx.x / kLpr;
+  const uint32_t planes = static_cast<uint32_t>(a.B) * a.H;
+  const int x = bhx >= planes ? 1 : 0;
+  const uint32_t bh = bhx - x * planes;
+  const int b = static_cast<int>(bh / static_cast<uint32_t>(a.H));
+  const int h = static_cast<int>(bh) - b * a.H;
+  const int start = a.start[b];
+  const int n = a.lengths != nullptr ? min(a.L, a.lengths[b]) : a.L;
   const int e = x * INTATTN_MAX_HEADS + (a.per_head ? h : 0);
   const float s = a.scale[e];
   const bool asym = x ? a.asym_v : a.asym_k;
   const int32_t z = asym ? a.zero[e] : 0;
-  const int64_t src = (bh * a.Lmax + slot) * D + 16 * piece;  // channels
-  int32_t c[16];
-  if (a.bits == 8) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.in[x] + src));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint8_t* in = a.in[x];
+  uint2 raw[kReadUnroll];
+  bool ok[kReadUnroll];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const uint32_t u = (w[k / 4] >> (8 * (k % 4))) & 255u;
-      c[k] = asym ? static_cast<int32_t>(u) - z : static_cast<int32_t>(static_cast<int8_t>(u));
-    }
-  } else {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.in[x] + src / 2));
-    const uint32_t w[2] = {v.x, v.y};
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const uint32_t u = (w[k / 8] >> (4 * (k % 8))) & 15u;
-      c[k] = asym ? static_cast<int32_t>(u) - z : static_cast<int32_t>(u ^ 8u) - 8;
+  for (int u = 0; u < kReadUnroll; ++u) {
+    const int t = t0 + u * kStep;
+    const int64_t slot = static_cast<int64_t>(start) + t;
+    ok[u] = t < n && slot >= 0 && slot < a.Lmax;
+    if (t < n && !ok[u] && piece == 0) atomicOr(&g_device_error, kErrParamRange);
+    raw[u] = make_uint2(0, 0);
+    if (ok[u]) {
+      const int64_t at = (static_cast<int64_t>(bh) * a.Lmax + slot) * D + 8 * piece;  // channels
+      if (a.bits == 8) raw[u] = __ldg(reinterpret_cast<const uint2*>(in + at));
+      else raw[u].x = __ldg(reinterpret_cast<const uint32_t*>(in + at / 2));
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[x]) + row * D + 16 * piece);
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t o[4];
+  for (int u = 0; u < kReadUnroll; ++u) {
+    if (!ok[u]) continue;
+    float f[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      o[k] = pack_half2(__fmul_rn(s, static_cast<float>(c[8 * q + 2 * k])),
-                        __fmul_rn(s, static_cast<float>(c[8 * q + 2 * k + 1])), a.bf16);
-    dst[q] = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int k = 0; k < 8; ++k) {
+      int32_t c;
+      if (a.bits == 8) {
+        const uint32_t v = ((k < 4 ? raw[u].x : raw[u].y) >> (8 * (k & 3))) & 255u;
+        c = asym ? static_cast<int32_t>(v) - z : static_cast<int32_t>(static_cast<int8_t>(v));
+      } else {
+        const uint32_t v = (raw[u].x >> (4 * k)) & 15u;
+        c = asym ? static_cast<int32_t>(v) - z : static_cast<int32_t>(v ^ 8u) - 8;
+      }
+      f[k] = __fmul_rn(s, static_cast<float>(c));
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[x]) + (static_cast<int64_t>(bh) * a.L + t0 + u * kStep) * D +
+                              8 * piece) =
+        make_uint4(pack_half2(f[0], f[1], a.bf16), pack_half2(f[2], f[3], a.bf16), pack_half2(f[4], f[5], a.bf16),
+                   pack_half2(f[6], f[7], a.bf16));
   }
 }
 
