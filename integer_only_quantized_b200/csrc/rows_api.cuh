@@ -68,10 +68,9 @@ int rows_launch(RowArgs& a, int d, cudaStream_t st) {
   if (warps > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
   a.warps = static_cast<uint32_t>(warps);
   const unsigned grid = static_cast<unsigned>((warps + intattn::rows::kWarps - 1) / intattn::rows::kWarps);
-  if (d == 64)
-    intattn::rows::rows_kernel<64, kCodes><<<grid, intattn::rows::kThreads, 0, st>>>(a);
-  else
-    intattn::rows::rows_kernel<128, kCodes><<<grid, intattn::rows::kThreads, 0, st>>>(a);
+  auto* kernel = d == 64 ? (a.bf16 ? intattn::rows::rows_kernel<64, kCodes, true> : intattn::rows::rows_kernel<64, kCodes, false>)
+                         : (a.bf16 ? intattn::rows::rows_kernel<128, kCodes, true> : intattn::rows::rows_kernel<128, kCodes, false>);
+  kernel<<<grid, intattn::rows::kThreads, 0, st>>>(a);
   return note_launch(cudaGetLastError());
 }
 

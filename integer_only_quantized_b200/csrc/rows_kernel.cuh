@@ -82,28 +82,27 @@ constexpr int kWarps = kThreads / 32;
 // byte of each word.  Adding 1.5 * 2^23 rounds to an integer with ties to even
 // and leaves it in the sum's low bits; infinities and values past the range end at
 // lo or hi, NaN gives z.
-__device__ __forceinline__ void codes4(const float (&y)[4], float inv, float lo, float hi, int32_t z, uint32_t (&c)[4]) {
+__device__ __forceinline__ void codes4(const float2 (&y)[2], float inv, float lo, float hi, int32_t z, uint32_t (&c)[4]) {
+  const float p[4] = {__fmul_rn(y[0].x, inv), __fmul_rn(y[0].y, inv), __fmul_rn(y[1].x, inv), __fmul_rn(y[1].y, inv)};
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float p = __fmul_rn(y[i], inv);
-    nan |= !(p == p);
-    c[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(p, lo), hi), 12582912.0f)) + static_cast<uint32_t>(z);
+    nan |= !(p[i] == p[i]);
+    c[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(p[i], lo), hi), 12582912.0f)) + static_cast<uint32_t>(z);
   }
   if (nan) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p = __fmul_rn(y[i], inv);
-      if (!(p == p)) c[i] = static_cast<uint32_t>(z);
-    }
+    for (int i = 0; i < 4; ++i)
+      if (!(p[i] == p[i])) c[i] = static_cast<uint32_t>(z);
   }
 }
 
-__device__ __forceinline__ void to_float4(uint2 v, bool bf16, float (&f)[4]) {
+template <bool kBf16>
+__device__ __forceinline__ void to_float4(uint2 v, float (&f)[4]) {
   const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    if (bf16) {
+    if (kBf16) {
       f[2 * i] = __uint_as_float(w[i] << 16);  // bf16 = high half of an fp32
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     } else {
@@ -123,8 +122,30 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b, bool bf16) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two fp32 operations in one instruction: (a0, a1) * (b0, b1), and + (c0, c1).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // kCodes: the output is codes; else fp16 / bf16.
-template <int D, bool kCodes>
+template <int D, bool kCodes, bool kBf16>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a) {
   constexpr int kLpr = D / 8;           // lanes per row
   constexpr int kRpw = 32 / kLpr;       // rows (heads) per warp and load
@@ -151,15 +172,15 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   const int g1 = split && turn ? 4 * piece + a.rot / 2 : 8 * piece + 4;
 
   // the rows first: nothing below is needed for them
-  const uint16_t* in = static_cast<const uint16_t*>(rt.in) + b * rt.isb + t * rt.isl;
+  const uint16_t* in = static_cast<const uint16_t*>(rt.in) + b * rt.isb + t * rt.isl + (h0 + sub) * rt.ish + g0;
+  const int64_t in_step = kRpw * rt.ish;
   uint2 raw[kUnroll][2];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int h = h0 + u * kRpw + sub;
+  for (int u = 0; u < kUnroll; ++u, in += in_step) {
     raw[u][0] = raw[u][1] = make_uint2(0, 0);
-    if (h < h1) {
-      raw[u][0] = *reinterpret_cast<const uint2*>(in + h * rt.ish + g0);
-      raw[u][1] = *reinterpret_cast<const uint2*>(in + h * rt.ish + g1);
+    if (h0 + u * kRpw + sub < h1) {
+      raw[u][0] = *reinterpret_cast<const uint2*>(in);
+      raw[u][1] = *reinterpret_cast<const uint2*>(in + (g1 - g0));
     }
   }
 
@@ -175,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   }
   // cos and sin of the lane's four pairs: split, pair i is channels g0 + i and
   // g1 + i; interleaved, pairs 0 and 1 lie in the first group, 2 and 3 in the second
-  float4 cs[2] = {};
+  float2 cs[2], sn[2];
   if (a.positions != nullptr) {
     const int pos = a.positions[token];
     if (pos < 0) return;  // a padded row
@@ -185,63 +206,73 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     }
     if (turn) {
       const float4* p = reinterpret_cast<const float4*>(a.table + static_cast<int64_t>(pos) * (a.rot / 2) + 4 * piece);
-      cs[0] = __ldg(p);
-      cs[1] = __ldg(p + 1);
-    }
-  }
-  float4 w[2] = {};
-  if (rt.w != nullptr) {
-    w[0] = __ldg(reinterpret_cast<const float4*>(rt.w + g0));
-    w[1] = __ldg(reinterpret_cast<const float4*>(rt.w + g1));
-  }
-  uint8_t* out8 = static_cast<uint8_t*>(rt.out);
-  const int64_t base = b * rt.osb + static_cast<int64_t>(row) * rt.osl;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    if (h0 + u * kRpw >= h1) break;  // uniform over the warp
-    const int h = h0 + u * kRpw + sub;
-    float y[2][4];
-    to_float4(raw[u][0], a.bf16, y[0]);
-    to_float4(raw[u][1], a.bf16, y[1]);
-    if (rt.w != nullptr) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ss = fmaf(y[1][i], y[1][i], fmaf(y[0][i], y[0][i], ss));
-#pragma unroll
-      for (int o = kLpr / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = __frsqrt_rn(fmaf(ss, 1.0f / D, a.eps));
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        y[g][0] = y[g][0] * r * w[g].x;
-        y[g][1] = y[g][1] * r * w[g].y;
-        y[g][2] = y[g][2] * r * w[g].z;
-        y[g][3] = y[g][3] * r * w[g].w;
+      for (int i = 0; i < 2; ++i) {
+        const float4 v = __ldg(p + i);
+        cs[i] = make_float2(v.x, v.z);
+        sn[i] = make_float2(v.y, v.w);
       }
     }
+  }
+  float2 w[2][2];
+  if (rt.w != nullptr) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(rt.w + (g ? g1 : g0)));
+      w[g][0] = make_float2(v.x, v.y);
+      w[g][1] = make_float2(v.z, v.w);
+    }
+  }
+  int64_t at = b * rt.osb + static_cast<int64_t>(row) * rt.osl + (h0 + sub) * rt.osh + g0;
+  const int64_t out_step = kRpw * rt.osh;
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u, at += out_step) {
+    if (h0 + u * kRpw >= h1) break;  // uniform over the warp
+    const int h = h0 + u * kRpw + sub;
+    float f[2][4];
+    to_float4<kBf16>(raw[u][0], f[0]);
+    to_float4<kBf16>(raw[u][1], f[1]);
+    float2 y[2][2] = {{make_float2(f[0][0], f[0][1]), make_float2(f[0][2], f[0][3])},
+                      {make_float2(f[1][0], f[1][1]), make_float2(f[1][2], f[1][3])}};
+    if (rt.w != nullptr) {
+      float2 sq = mul2(y[0][0], y[0][0]);
+      sq = fma2(y[0][1], y[0][1], sq);
+      sq = fma2(y[1][0], y[1][0], sq);
+      sq = fma2(y[1][1], y[1][1], sq);
+      float ss = sq.x + sq.y;
+#pragma unroll
+      for (int o = kLpr / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = rsqrtf(fmaf(ss, 1.0f / D, a.eps));  // within 2 units in the last place
+      const float2 rr = make_float2(r, r);
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y[g][i] = mul2(mul2(y[g][i], rr), w[g][i]);
+    }
     if (turn) {
-      auto rotate = [](float& p, float& q, float c, float s) {
-        const float x0 = p, x1 = q;
-        p = fmaf(x0, c, -(x1 * s));
-        q = fmaf(x1, c, x0 * s);
-      };
       if (split) {
-        rotate(y[0][0], y[1][0], cs[0].x, cs[0].y);
-        rotate(y[0][1], y[1][1], cs[0].z, cs[0].w);
-        rotate(y[0][2], y[1][2], cs[1].x, cs[1].y);
-        rotate(y[0][3], y[1][3], cs[1].z, cs[1].w);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 p = y[0][i], q = y[1][i], m = mul2(q, sn[i]);
+          y[0][i] = fma2(p, cs[i], make_float2(-m.x, -m.y));
+          y[1][i] = fma2(q, cs[i], mul2(p, sn[i]));
+        }
       } else {
-        rotate(y[0][0], y[0][1], cs[0].x, cs[0].y);
-        rotate(y[0][2], y[0][3], cs[0].z, cs[0].w);
-        rotate(y[1][0], y[1][1], cs[1].x, cs[1].y);
-        rotate(y[1][2], y[1][3], cs[1].z, cs[1].w);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float2 p = y[g][0], q = y[g][1], c = cs[g], s = sn[g];
+          y[g][0] = make_float2(fmaf(p.x, c.x, -(p.y * s.x)), fmaf(p.y, c.x, p.x * s.x));
+          y[g][1] = make_float2(fmaf(q.x, c.y, -(q.y * s.y)), fmaf(q.y, c.y, q.x * s.y));
+        }
       }
     }
     if (h >= h1) continue;
-    const int64_t at = base + h * rt.osh;
     if constexpr (!kCodes) {
       uint16_t* dst = static_cast<uint16_t*>(rt.out) + at;
-      *reinterpret_cast<uint2*>(dst + g0) = make_uint2(pack_half2(y[0][0], y[0][1], a.bf16), pack_half2(y[0][2], y[0][3], a.bf16));
-      *reinterpret_cast<uint2*>(dst + g1) = make_uint2(pack_half2(y[1][0], y[1][1], a.bf16), pack_half2(y[1][2], y[1][3], a.bf16));
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        *reinterpret_cast<uint2*>(dst + (g ? g1 - g0 : 0)) =
+            make_uint2(pack_half2(y[g][0].x, y[g][0].y, kBf16), pack_half2(y[g][1].x, y[g][1].y, kBf16));
     } else {
       const int e = rt.sc + (a.per_head ? h : 0);
       const int32_t z = rt.asym ? a.zero[e] : 0;
@@ -251,12 +282,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       for (int g = 0; g < 2; ++g) {
         uint32_t c[4];
         codes4(y[g], a.inv[e], lo, hi, z, c);
-        const int64_t to = at + (g ? g1 : g0);
+        const int64_t to = at + (g ? g1 - g0 : 0);
         if (rt.bits == 8) {
-          *reinterpret_cast<uint32_t*>(out8 + to) =
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(rt.out) + to) =
               __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
         } else {  // channel 2t in the low nibble of byte t
-          *reinterpret_cast<uint16_t*>(out8 + to / 2) = static_cast<uint16_t>(
+          *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(rt.out) + to / 2) = static_cast<uint16_t>(
               (c[0] & 15u) | ((c[1] & 15u) << 4) | ((c[2] & 15u) << 8) | ((c[3] & 15u) << 12));
         }
       }
