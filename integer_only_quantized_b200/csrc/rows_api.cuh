@@ -55,19 +55,22 @@ int rows_launch(RowArgs& a, int d, cudaStream_t st) {
   if (sm_count(&sms) != INTATTN_OK) return INTATTN_ERR_CUDA;
   const int per_load = 256 / d;
   const long long tokens = static_cast<long long>(a.B) * a.L;
+  if (tokens > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
+  a.tokens = static_cast<uint32_t>(tokens);
+  long long most = 0;
   for (a.batch = 4 * per_load;; a.batch = per_load) {
-    a.warps_per_token = 0;
-    a.first[0] = a.first[1] = a.first[2] = INT32_MAX;  // tensors that are not there have no warps
+    long long warps = 0;
+    most = 0;
     for (int i = 0; i < a.n_tensors; ++i) {
-      a.first[i] = a.warps_per_token;
-      a.warps_per_token += (a.t[i].heads + a.batch - 1) / a.batch;
+      a.t[i].warps = (a.t[i].heads + a.batch - 1) / a.batch;
+      warps += tokens * a.t[i].warps;
+      most = std::max(most, tokens * a.t[i].warps);
     }
-    if (a.batch == per_load || tokens * a.warps_per_token >= 8ll * sms) break;
+    if (a.batch == per_load || warps >= 8ll * sms) break;
   }
-  const long long warps = tokens * a.warps_per_token;
-  if (warps > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
-  a.warps = static_cast<uint32_t>(warps);
-  const unsigned grid = static_cast<unsigned>((warps + intattn::rows::kWarps - 1) / intattn::rows::kWarps);
+  if (most > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>((most + intattn::rows::kWarps - 1) / intattn::rows::kWarps),
+                  static_cast<unsigned>(a.n_tensors));
   auto* kernel = d == 64 ? (a.bf16 ? intattn::rows::rows_kernel<64, kCodes, true> : intattn::rows::rows_kernel<64, kCodes, false>)
                          : (a.bf16 ? intattn::rows::rows_kernel<128, kCodes, true> : intattn::rows::rows_kernel<128, kCodes, false>);
   kernel<<<grid, intattn::rows::kThreads, 0, st>>>(a);
@@ -75,14 +78,14 @@ int rows_launch(RowArgs& a, int d, cudaStream_t st) {
 }
 
 // Scales and zero-points of one tensor's heads: RN32(1 / s), or s itself.
-int code_params(const float* s, const int32_t* z, int n, int bits, bool reciprocal, float* out, uint8_t* zero) {
+int code_params(const float* s, const int32_t* z, int n, int bits, bool reciprocal, float* out, float* zero) {
   if (!s) return INTATTN_ERR_INVALID_ARG;
   for (int i = 0; i < n; ++i) {
     if (!std::isfinite(s[i]) || !(s[i] > 0.0f)) return INTATTN_ERR_PARAM_RANGE;
     out[i] = reciprocal ? std::min(1.0f / s[i], 3.402823466e38f) : s[i];
     if (z) {
       if (z[i] < 0 || z[i] >= (1 << bits)) return INTATTN_ERR_INVALID_ARG;
-      zero[i] = static_cast<uint8_t>(z[i]);
+      zero[i] = static_cast<float>(z[i]);
     }
   }
   return INTATTN_OK;
@@ -169,7 +172,9 @@ int intattn_cache_write(const intattn_rows_t* k, const intattn_rows_t* v, const 
     t.rope = i != 1;
     t.cache = i < 2;
     t.bits = i < 2 ? bits : 8;
-    t.asym = i == 0 ? scales->z_k != nullptr : i == 1 ? scales->z_v != nullptr : 0;
+    const bool asym = (i == 0 && scales->z_k) || (i == 1 && scales->z_v);
+    t.hi = static_cast<float>(asym ? (1 << t.bits) - 1 : (1 << (t.bits - 1)) - 1);
+    t.lo = asym ? 0.0f : -t.hi;
     t.sc = i * S;
   }
   a.B = B;
@@ -225,10 +230,9 @@ int intattn_cache_read(const void* k_cache, const void* v_cache, const intattn_s
   const long long grid = static_cast<long long>(a.chunks) * B * Hkv * a.n_tensors;
   if (grid > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (d == 64)
-    intattn::rows::read_kernel<64><<<static_cast<unsigned>(grid), intattn::rows::kReadThreads, 0, st>>>(a);
-  else
-    intattn::rows::read_kernel<128><<<static_cast<unsigned>(grid), intattn::rows::kReadThreads, 0, st>>>(a);
+  auto* kernel = d == 64 ? (a.bf16 ? intattn::rows::read_kernel<64, true> : intattn::rows::read_kernel<64, false>)
+                         : (a.bf16 ? intattn::rows::read_kernel<128, true> : intattn::rows::read_kernel<128, false>);
+  kernel<<<static_cast<unsigned>(grid), intattn::rows::kReadThreads, 0, st>>>(a);
   return note_launch(cudaGetLastError());
 }
 

@@ -40,18 +40,17 @@ struct RowTensor {
   int32_t rope;           // rotate
   int32_t cache;          // output row = start[b] + t, checked against Lmax; else t
   int32_t bits;           // codes: 8 or 4; unused for fp output
-  int32_t asym;           // codes: unsigned with zero-points
+  float lo, hi;           // codes: their range
   int32_t sc;             // codes: first entry of the call's scale arrays
+  int32_t warps;          // per token: ceil(heads / batch)
 };
 
 struct RowArgs {
   RowTensor t[3];              // heads of tensor 0, then 1, then 2
   int32_t n_tensors;
   int32_t B, L, Lmax, bf16, per_head;
-  int32_t batch;               // heads of one token and tensor that a warp handles
-  int32_t first[3];            // a token's warps: tensor x has first[x] .. first[x + 1] - 1
-  int32_t warps_per_token;
-  uint32_t warps;              // B * L * warps_per_token
+  int32_t batch;               // heads of one token that a warp handles
+  uint32_t tokens;             // B * L
   const int32_t* start;        // [B] first cache row, or null
   const int32_t* lengths;      // [B] rows of each sequence, or null: all L
   const int32_t* positions;    // [B, L], or null: no rotation
@@ -59,7 +58,7 @@ struct RowArgs {
   int32_t n_positions, rot, interleaved;
   float eps;
   float inv[3 * INTATTN_MAX_HEADS];    // codes: RN32(1 / scale)
-  uint8_t zero[3 * INTATTN_MAX_HEADS];
+  float zero[3 * INTATTN_MAX_HEADS];   // zero-points (0: symmetric)
 };
 
 struct ReadArgs {
@@ -70,32 +69,13 @@ struct ReadArgs {
   const int32_t* start;
   const int32_t* lengths;
   float scale[2 * INTATTN_MAX_HEADS];
-  uint8_t zero[2 * INTATTN_MAX_HEADS];
+  float zero[2 * INTATTN_MAX_HEADS];
 };
 
 namespace rows {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-
-// rint(RN32(y inv)) of four values, clamped to [lo, hi], plus z, in the low
-// byte of each word.  Adding 1.5 * 2^23 rounds to an integer with ties to even
-// and leaves it in the sum's low bits; infinities and values past the range end at
-// lo or hi, NaN gives z.
-__device__ __forceinline__ void codes4(const float2 (&y)[2], float inv, float lo, float hi, int32_t z, uint32_t (&c)[4]) {
-  const float p[4] = {__fmul_rn(y[0].x, inv), __fmul_rn(y[0].y, inv), __fmul_rn(y[1].x, inv), __fmul_rn(y[1].y, inv)};
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    nan |= !(p[i] == p[i]);
-    c[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(p[i], lo), hi), 12582912.0f)) + static_cast<uint32_t>(z);
-  }
-  if (nan) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!(p[i] == p[i])) c[i] = static_cast<uint32_t>(z);
-  }
-}
 
 template <bool kBf16>
 __device__ __forceinline__ void to_float4(uint2 v, float (&f)[4]) {
@@ -144,6 +124,35 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// clamp(rint(RN32(y inv)), lo, hi) + z of four values, in the low byte of
+// each word.  Adding 1.5 * 2^23 rounds to an integer with ties to even and leaves it in
+// the sum's low bits; z is a whole number, so adding it is exact.  Infinities
+// end at lo or hi; a NaN gives z (`careful`: there may be one).
+__device__ __forceinline__ void codes4(const float2 (&y)[2], float inv, float lo, float hi, float z, bool careful,
+                                       uint32_t (&c)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 p = mul2(y[i], both(inv));
+    float2 q = make_float2(fminf(fmaxf(p.x, lo), hi), fminf(fmaxf(p.y, lo), hi));
+    if (careful) q = make_float2(p.x == p.x ? q.x : 0.f, p.y == p.y ? q.y : 0.f);
+    q = add2(add2(q, both(12582912.0f)), both(z));
+    c[2 * i] = __float_as_uint(q.x);
+    c[2 * i + 1] = __float_as_uint(q.y);
+  }
+}
+
 // kCodes: the output is codes; else fp16 / bf16.
 template <int D, bool kCodes, bool kBf16>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a) {
@@ -153,13 +162,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   const int lane = threadIdx.x & 31;
   const int piece = lane % kLpr;
   const int sub = lane / kLpr;
+  const RowTensor& rt = a.t[blockIdx.y];
   const uint32_t id = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (id >= a.warps) return;
-  const uint32_t token = id / static_cast<uint32_t>(a.warps_per_token);
-  const int k = static_cast<int>(id - token * a.warps_per_token);
-  const int x = k >= a.first[2] ? 2 : k >= a.first[1] ? 1 : 0;
-  const RowTensor& rt = a.t[x];
-  const int h0 = (k - a.first[x]) * a.batch;
+  const uint32_t token = id / static_cast<uint32_t>(rt.warps);
+  if (token >= a.tokens) return;
+  const int h0 = static_cast<int>(id - token * rt.warps) * a.batch;
   const int h1 = min(rt.heads, h0 + a.batch);
   const int b = static_cast<int>(token / static_cast<uint32_t>(a.L));
   const int t = static_cast<int>(token) - b * a.L;
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   }
   // cos and sin of the lane's four pairs: split, pair i is channels g0 + i and
   // g1 + i; interleaved, pairs 0 and 1 lie in the first group, 2 and 3 in the second
-  float2 cs[2], sn[2];
+  float2 cs[2], sn[2], ns[2];  // ns: -sin
   if (a.positions != nullptr) {
     const int pos = a.positions[token];
     if (pos < 0) return;  // a padded row
@@ -211,6 +218,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
         const float4 v = __ldg(p + i);
         cs[i] = make_float2(v.x, v.z);
         sn[i] = make_float2(v.y, v.w);
+        ns[i] = make_float2(-v.y, -v.w);
       }
     }
   }
@@ -253,9 +261,9 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       if (split) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 p = y[0][i], q = y[1][i], m = mul2(q, sn[i]);
-          y[0][i] = fma2(p, cs[i], make_float2(-m.x, -m.y));
-          y[1][i] = fma2(q, cs[i], mul2(p, sn[i]));
+          const float2 p = y[0][i], q = y[1][i];
+          y[0][i] = fma2(q, ns[i], mul2(p, cs[i]));
+          y[1][i] = fma2(p, sn[i], mul2(q, cs[i]));
         }
       } else {
 #pragma unroll
@@ -275,13 +283,15 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
             make_uint2(pack_half2(y[g][0].x, y[g][0].y, kBf16), pack_half2(y[g][1].x, y[g][1].y, kBf16));
     } else {
       const int e = rt.sc + (a.per_head ? h : 0);
-      const int32_t z = rt.asym ? a.zero[e] : 0;
-      const int32_t top = rt.asym ? (1 << rt.bits) - 1 : (1 << (rt.bits - 1)) - 1;
-      const float lo = static_cast<float>(rt.asym ? -z : -top), hi = static_cast<float>(top - z);
+      const float inv = a.inv[e], z = a.zero[e];
+      const float lo = rt.lo - z, hi = rt.hi - z;
+      // no NaN among the eight values (an infinity may say so too)
+      const float2 sum = add2(add2(y[0][0], y[0][1]), add2(y[1][0], y[1][1]));
+      const bool careful = !(fabsf(sum.x + sum.y) < 3.402823466e38f);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t c[4];
-        codes4(y[g], a.inv[e], lo, hi, z, c);
+        codes4(y[g], inv, lo, hi, z, careful, c);
         const int64_t to = at + (g ? g1 - g0 : 0);
         if (rt.bits == 8) {
           *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(rt.out) + to) =
@@ -299,8 +309,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 // load of int8 codes, 4 bytes of int4 codes; one 16-byte store, so that a warp's store is one
 // contiguous run), of kUnroll rows.
 constexpr int kReadThreads = 256;
-constexpr int kReadUnroll = 8;
-template <int D>
+constexpr int kReadUnroll = 4;
+template <int D, bool kBf16>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int kLpr = D / 8;
   constexpr int kStep = kReadThreads / kLpr;      // rows per load
@@ -318,7 +328,10 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
   const int e = x * INTATTN_MAX_HEADS + (a.per_head ? h : 0);
   const float s = a.scale[e];
   const bool asym = x ? a.asym_v : a.asym_k;
-  const int32_t z = asym ? a.zero[e] : 0;
+  // A code as an unsigned byte u (two's complement: its sign bit flipped) is
+  // the float 2^23 + u with u in the low byte; `off` takes 2^23, the flip and z from it.
+  const uint32_t flip = asym ? 0u : a.bits == 8 ? 0x80808080u : 0x08080808u;
+  const float off = -(8388608.0f + (asym ? a.zero[e] : a.bits == 8 ? 128.0f : 8.0f));
   const uint8_t* in = a.in[x];
   uint2 raw[kReadUnroll];
   bool ok[kReadUnroll];
@@ -338,23 +351,31 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
 #pragma unroll
   for (int u = 0; u < kReadUnroll; ++u) {
     if (!ok[u]) continue;
-    float f[8];
+    // u words: bytes in the order of the channels (8 bits), or even and odd channels (4 bits)
+    uint32_t u0 = raw[u].x ^ flip, u1 = raw[u].y ^ flip;
+    if (a.bits == 4) {
+      u1 = (raw[u].x >> 4 & 0x0F0F0F0Fu) ^ flip;
+      u0 = (raw[u].x & 0x0F0F0F0Fu) ^ flip;
+    }
+    uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      int32_t c;
+    for (int k = 0; k < 4; ++k) {
+      // channels 2k and 2k + 1
+      uint32_t x0, x1;
       if (a.bits == 8) {
-        const uint32_t v = ((k < 4 ? raw[u].x : raw[u].y) >> (8 * (k & 3))) & 255u;
-        c = asym ? static_cast<int32_t>(v) - z : static_cast<int32_t>(static_cast<int8_t>(v));
+        const uint32_t v = k < 2 ? u0 : u1;
+        x0 = __byte_perm(v, 0x4B000000u, 0x7650 + 2 * (k & 1));
+        x1 = __byte_perm(v, 0x4B000000u, 0x7651 + 2 * (k & 1));
       } else {
-        const uint32_t v = (raw[u].x >> (4 * k)) & 15u;
-        c = asym ? static_cast<int32_t>(v) - z : static_cast<int32_t>(v ^ 8u) - 8;
+        x0 = __byte_perm(u0, 0x4B000000u, 0x7650 + k);
+        x1 = __byte_perm(u1, 0x4B000000u, 0x7650 + k);
       }
-      f[k] = __fmul_rn(s, static_cast<float>(c));
+      // the sum is a whole number and exact; a product of it and then one rounding to 16 bits
+      const float2 f = mul2(add2(make_float2(__uint_as_float(x0), __uint_as_float(x1)), both(off)), both(s));
+      o[k] = pack_half2(f.x, f.y, kBf16);
     }
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[x]) + (static_cast<int64_t>(bh) * a.L + t0 + u * kStep) * D +
-                              8 * piece) =
-        make_uint4(pack_half2(f[0], f[1], a.bf16), pack_half2(f[2], f[3], a.bf16), pack_half2(f[4], f[5], a.bf16),
-                   pack_half2(f[6], f[7], a.bf16));
+                              8 * piece) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
