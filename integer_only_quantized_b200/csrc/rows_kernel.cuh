@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 // Values s (c - z) of cache rows.  A lane takes eight channels of a row (an 8-byte
 // load of int8 codes, 4 bytes of int4 codes; one 16-byte store, so that a warp's store is one
 // contiguous run), of kUnroll rows.
-constexpr int kReadThreads = 256;
+constexpr int kReadThreads = 128;
 constexpr int kReadUnroll = 4;
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadArgs a) {

@@ -180,6 +180,13 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   if (Lmax > 0 && (!encode_rows(&a.tm_kc, k_cache, d, Lmax, Lmax, planes, intattn::shared::kOwnBytes / d) ||
                    !encode_rows(&a.tm_vc, v_cache, d, Lmax, Lmax, planes, intattn::shared::kOwnBytes / d)))
     return INTATTN_ERR_CUDA;
+  // The K / V ring and the own warps' rings share their memory (kRingBytes):
+  // one block per own warp instead of two where the prefix is the longer stream
+  // (B9 H32/8 over 50000 shared and up to 333 own keys: @@ us against @@).
+  const long long own_keys = static_cast<long long>(B) * Hkv * Lmax, prefix_keys = static_cast<long long>(Hkv) * Lp;
+  a.own_slots = Lmax == 0 ? 0 : 2 * own_keys <= prefix_keys ? 1 : 2;
+  a.stages = (intattn::shared::kRingBytes - a.own_slots * intattn::shared::kOwnWarps * intattn::shared::kOwnBytes) /
+             (intattn::shared::kBN * d);
   // as many CTAs as there are prefix tiles or 128-key pieces of own rows
   const long long own = static_cast<long long>(B) * Hkv * ((Lmax + 127) / 128);
   const int grid = static_cast<int>(std::min<long long>(sms, std::max<long long>(std::max(tiles, own), 1)));

@@ -74,6 +74,7 @@ struct SharedArgs {
   uint32_t* index;            // [B H, ld_s / 4] their table indices, a byte each
   int32_t B, H, Hkv, G, R, Lp, Lmax, ld_s, per_head, out_kind, k_u8, v_u8, n_luts;
   int32_t fold;                  // F: key tiles per tile of 128 lanes
+  int32_t stages, own_slots;     // of the K / V ring and of each own warp's ring (see kRingBytes)
   int32_t key_tiles;             // 128-key tiles of the prefix
   int32_t row_tiles, seg_tiles;  // 128-row tiles of R; tiles per (head, row tile): ceil(key_tiles / F)
   int32_t tiles;                 // Hkv * row_tiles * seg_tiles
@@ -102,7 +103,10 @@ constexpr int kQWarp = 18;                 // warps 18-19: Q rows into shared me
 constexpr int kOwnWarp0 = 20;              // warps 20-27: own rows
 constexpr int kOwnWarps = 8;
 constexpr int kOwnBytes = 4096;            // bytes of an own-row block
-constexpr int kOwnSlots = 2;               // blocks in an own warp's ring
+// K / V tiles of the prefix and the own warps' rings share these bytes: with S
+// slots per own warp (0, 1 or 2) the prefix has (kRingBytes - 32 KB S) / tile stages
+constexpr int kRingBytes = 144 * 1024;
+constexpr int kMaxOwnSlots = 2;
 constexpr int kThreads = 32 * (kOwnWarp0 + kOwnWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;              // two S buffers
@@ -124,32 +128,31 @@ enum Bar : int {
   kBarOFull = 16,
   kBarOEmpty = 17,
   kBarDrain = 18,
-  kBarOwn = 19,     // [kOwnWarps][kOwnSlots]
-  kBarKvFull = kBarOwn + kOwnWarps * kOwnSlots,  // [stages], then kv_empty[stages]
+  kBarOwn = 19,     // [kOwnWarps][kMaxOwnSlots]
+  kBarKvFull = kBarOwn + kOwnWarps * kMaxOwnSlots,  // [kMaxStages], then kv_empty[kMaxStages]
 };
 
 template <int D>
 struct Cfg {
-  static constexpr int kStages = (D == 64) ? 8 : 5;
   static constexpr uint32_t kTileBytes = kBN * D;
+  static constexpr int kMaxStages = kRingBytes / kTileBytes;
   static constexpr uint32_t kSwizzle = (D == 128) ? 2u : 4u;  // 128B / 64B swizzle
   static constexpr uint32_t kSBO = 8 * D;
-  static constexpr int kNumBars = kBarKvFull + 2 * kStages;
+  static constexpr int kNumBars = kBarKvFull + 2 * kMaxStages;
   // Q rows: buffer i at row 128 - 128 / F + 128 i, the other rows zero (F > 1)
   static constexpr int kQRows = 352;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffKV = kOffQ + kQRows * D;
-  static constexpr uint32_t kOffOwn = kOffKV + kStages * kTileBytes;
   // per-row tables [33][kBM] u32, row k for index code k (see idx_bits2; 1 .. 32): in
   // phase B the first holds LUT, in phase C table b holds P << 8b
   static constexpr uint32_t kTabBytes = 33 * kBM * 4;
-  static constexpr uint32_t kOffTab = kOffOwn + kOwnWarps * kOwnSlots * kOwnBytes;
+  static constexpr uint32_t kOffTab = kOffKV + kRingBytes;
   static constexpr uint32_t kOffLut = kOffTab + 2 * kTabBytes;
   static constexpr uint32_t kOffHp = kOffLut + INTATTN_MAX_CLIPS * 32 * 4;
   static constexpr uint32_t kOffBars = kOffHp + INTATTN_MAX_HEADS * sizeof(HeadParamsDev);
   static constexpr uint32_t kOffMisc = kOffBars + kNumBars * 8;  // TMEM address, barrier verdict
   static constexpr uint32_t kUsed = kOffMisc + 16;
-  static_assert(kOffKV % 1024 == 0 && kOffOwn % 1024 == 0, "swizzled tiles");
+  static_assert(kOffKV % 1024 == 0, "swizzled tiles");
   // one CTA per SM: every CTA takes all 512 TMEM columns
   // (dynamic shared memory starts on 128 bytes: at most 896 go to the alignment)
   static constexpr uint32_t kSmemBytes = (kUsed + 896 > 120 * 1024) ? kUsed + 896 : 120 * 1024;
@@ -307,9 +310,10 @@ struct Unit {
 // A warp's private ring of blocks for the own rows' tiles.
 struct OwnRing {
   uint32_t base, bar;    // shared addresses: slot i at base + kOwnBytes i, barrier i at bar + 8 i
-  uint32_t issued, used; // tiles, both counted over the slots as 2 kOwnSlots states
-  static __device__ __forceinline__ uint32_t step(uint32_t n) { return n + 1 == 2 * kOwnSlots ? 0u : n + 1; }
-  static __device__ __forceinline__ uint32_t slot(uint32_t n) { return n < kOwnSlots ? n : n - kOwnSlots; }
+  uint32_t slots;
+  uint32_t issued, used; // tiles, both counted over the slots as 2 slots states
+  __device__ __forceinline__ uint32_t step(uint32_t n) const { return n + 1 == 2 * slots ? 0u : n + 1; }
+  __device__ __forceinline__ uint32_t slot(uint32_t n) const { return n < slots ? n : n - slots; }
   __device__ __forceinline__ void issue(const CUtensorMap* tm, int y, int z) {
     const uint32_t i = slot(issued);
     tma_load_3d_elect(base + kOwnBytes * i, tm, bar + 8 * i, kOwnBytes, 0, y, z);
@@ -318,7 +322,7 @@ struct OwnRing {
   // the oldest tile not yet used (its address), or 0 when the wait ran out
   __device__ __forceinline__ uint32_t wait() {
     const uint32_t i = slot(used);
-    const bool ok = mbar_wait_warp(bar + 8 * i, used >= kOwnSlots ? 1u : 0u, kRoleOwn);
+    const bool ok = mbar_wait_warp(bar + 8 * i, used >= slots ? 1u : 0u, kRoleOwn);
     used = step(used);
     return ok ? base + kOwnBytes * i : 0u;
   }
@@ -369,7 +373,7 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
     if (--left > 0) ld.next(a, kKeys);
   };
 #pragma unroll 1
-  for (int i = 0; i < kOwnSlots; ++i)
+  for (uint32_t i = 0; i < ring.slots; ++i)
     if (left > 0) issue();
   uint32_t k[kK][4];  // fragments of the next step
   uint32_t tile = 0;
@@ -525,7 +529,7 @@ __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDe
 template <int D>
 __device__ __forceinline__ int own_pv_start(const SharedArgs& a, OwnRing& ring, Walk& ld, int n) {
 #pragma unroll 1
-  for (int i = 0; i < kOwnSlots && n > 0; ++i) {
+  for (uint32_t i = 0; i < ring.slots && n > 0; ++i) {
     ring.issue(&a.tm_vc, ld.blk * (kOwnBytes / D), ld.b * a.Hkv + ld.hk);
     if (--n > 0) ld.next(a, kOwnBytes / D);
   }
@@ -682,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   volatile uint32_t* verdict = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   auto bar_kv_full = [&](int i) { return bar(kBarKvFull + i); };
-  auto bar_kv_empty = [&](int i) { return bar(kBarKvFull + C::kStages + i); };
+  auto bar_kv_empty = [&](int i) { return bar(kBarKvFull + C::kMaxStages + i); };
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -694,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   const bool k_u8 = ZP && args.k_u8, v_u8 = ZP && args.v_u8;
   const int F = args.fold;
   const int RF = kBM / F;       // lanes per fold
+  const uint32_t stages = args.stages;  // at least 4: the key tiles of a tile fit the ring
   const int psets = kPBufs / F; // sets of F P buffers
   // this CTA's tiles
   const int t0 = static_cast<int>(static_cast<long long>(args.tiles) * blockIdx.x / gridDim.x);
@@ -716,8 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     mbar_init(bar(kBarOFull), 1);
     mbar_init(bar(kBarOEmpty), kSoftWarps);
     mbar_init(bar(kBarDrain), 1);
-    for (int i = 0; i < kOwnWarps * kOwnSlots; ++i) mbar_init(bar(kBarOwn + i), 1);
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < kOwnWarps * kMaxOwnSlots; ++i) mbar_init(bar(kBarOwn + i), 1);
+    for (int i = 0; i < C::kMaxStages; ++i) {
       mbar_init(bar_kv_full(i), 1);
       mbar_init(bar_kv_empty(i), 1);
     }
@@ -1040,7 +1045,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     // neighbouring shares on different CTAs
     const int n = args.Lmax > 0 ? w.share(args, kOwnBytes / D, ow * gridDim.x + blockIdx.x, kOwnWarps * gridDim.x)
                                 : 0;
-    OwnRing ring{s_base + C::kOffOwn + kOwnBytes * kOwnSlots * ow, bar(kBarOwn + kOwnSlots * ow), 0u, 0u};
+    const uint32_t own_slots = args.own_slots;
+    OwnRing ring{sKV + stages * C::kTileBytes + kOwnBytes * own_slots * ow, bar(kBarOwn + kMaxOwnSlots * ow), own_slots, 0u,
+                 0u};
     quant::griddep_wait();
     bool ok = own_scores<D>(args, k_u8, ring, w, n);
     if ((ok = grid_sync(0, ok))) {
@@ -1061,16 +1068,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       tma_prefetch_desc(&args.tm_v);
     }
     __syncwarp();
-    if (lane < C::kStages) {
+    if (static_cast<uint32_t>(lane) < stages) {
       const uint32_t slot = static_cast<uint32_t>(lane);
       const uint32_t dst = sKV + slot * C::kTileBytes;
-      uint32_t n = 0, mine = 0;
+      uint32_t n = 0, mine = 0;  // the next load's slot; loads of this lane
       bool ok = true;
       // the key tiles of tile j
       auto load = [&](const CUtensorMap* tm, int j, int hk) {
         const int nf = folds_at(args, j);
-        for (int x = 0; x < nf; ++x, ++n) {
-          if (!ok || n % C::kStages != slot) continue;
+        for (int x = 0; x < nf; ++x) {
+          const bool other = n != slot;
+          if (++n == stages) n = 0;
+          if (!ok || other) continue;
           if (!mbar_wait(bar_kv_empty(slot), (mine & 1) ^ 1, kRoleProducer)) {
             ok = false;
           } else {
@@ -1113,8 +1122,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       bool mine = lane <= nf;
       if (lane > 0) {
         const uint32_t s = slot + lane - 1;
-        const bool wraps = s >= static_cast<uint32_t>(C::kStages);
-        b = bar_kv_full(wraps ? s - C::kStages : s);
+        const bool wraps = s >= stages;
+        b = bar_kv_full(wraps ? s - stages : s);
         par = kv_par ^ (wraps ? 1u : 0u);
       }
       if (lane == 31 && more_bar != 0) {
@@ -1134,15 +1143,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         }
       }
     };
-    auto step = [](uint32_t s) { return s + 1 == static_cast<uint32_t>(C::kStages) ? 0u : s + 1; };
+    auto step = [&](uint32_t s) { return s + 1 == stages ? 0u : s + 1; };
     auto advance = [&](int nf) {
       slot += nf;
-      if (slot >= static_cast<uint32_t>(C::kStages)) {
-        slot -= C::kStages;
+      if (slot >= stages) {
+        slot -= stages;
         kv_par ^= 1;
       }
     };
-    static_assert(C::kStages >= 4, "the key tiles of a tile fit the ring");
     for (int phase = 0; phase < 3 && ok; ++phase) {
       if (q_stays) nq = 0;
       for (int t = t0; t < t1 && ok; ++nq) {
