@@ -98,8 +98,9 @@ constexpr int kSoftWarps = 16;
 constexpr int kTeamWarps = kSoftWarps / kTeams;
 constexpr int kCols = 64;                  // S columns per thread and tile (two halves)
 constexpr int kProducerWarp = 16;
-constexpr int kMmaWarp = 17;
-constexpr int kQWarp = 18;                 // warps 18-19: Q rows into shared memory
+constexpr int kMmaWarp = 17;               // issues S = Q.K^T
+constexpr int kPvWarp = 18;                // issues O += P.V
+constexpr int kQWarp = 19;                 // Q rows into shared memory
 constexpr int kOwnWarp0 = 20;              // warps 20-27: own rows
 constexpr int kOwnWarps = 8;
 constexpr int kOwnBytes = 4096;            // bytes of an own-row block
@@ -127,9 +128,9 @@ enum Bar : int {
   kBarPEmpty = 12,  // [4]
   kBarOFull = 16,
   kBarOEmpty = 17,
-  kBarDrain = 18,
-  kBarOwn = 19,     // [kOwnWarps][kMaxOwnSlots]
-  kBarKvFull = kBarOwn + kOwnWarps * kMaxOwnSlots,  // [kMaxStages], then kv_empty[kMaxStages]
+  kBarDrain = 18,   // [2]
+  kBarOwn = 20,     // [kOwnWarps][kMaxOwnSlots]
+  kBarKvFull = kBarOwn + kOwnWarps * kMaxOwnSlots,  // K [kMaxStages], V [kMaxStages], then kv_empty[kMaxStages]
 };
 
 template <int D>
@@ -138,7 +139,7 @@ struct Cfg {
   static constexpr int kMaxStages = kRingBytes / kTileBytes;
   static constexpr uint32_t kSwizzle = (D == 128) ? 2u : 4u;  // 128B / 64B swizzle
   static constexpr uint32_t kSBO = 8 * D;
-  static constexpr int kNumBars = kBarKvFull + 2 * kMaxStages;
+  static constexpr int kNumBars = kBarKvFull + 3 * kMaxStages;
   // Q rows: buffer i at row 128 - 128 / F + 128 i, the other rows zero (F > 1)
   static constexpr int kQRows = 352;
   static constexpr uint32_t kOffQ = 0;
@@ -685,8 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile uint32_t* verdict = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 4);
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
-  auto bar_kv_full = [&](int i) { return bar(kBarKvFull + i); };
-  auto bar_kv_empty = [&](int i) { return bar(kBarKvFull + C::kMaxStages + i); };
+  // A ring slot holds K tiles and V tiles in turn.  Each kind has a full barrier
+  // of its own: its consumer then waits for every phase of that barrier, one
+  // after the other, as a wait for a parity has to.
+  auto bar_full = [&](int v, int i) { return bar(kBarKvFull + v * C::kMaxStages + i); };
+  auto bar_kv_empty = [&](int i) { return bar(kBarKvFull + 2 * C::kMaxStages + i); };
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -705,11 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   const int t1 = static_cast<int>(static_cast<long long>(args.tiles) * (blockIdx.x + 1) / gridDim.x);
 
   // The queries of at most two segments stay in the two Q buffers through all
-  // phases, loaded by the softmax warps; of more, two warps load them again in every phase.
+  // phases, loaded by the softmax warps; of more, one warp loads them again in every phase.
   const bool q_stays = t0 < t1 && (t1 - 1) / args.seg_tiles - t0 / args.seg_tiles < 2;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarQFull + i), q_stays ? kSoftWarps : 2);
+      mbar_init(bar(kBarQFull + i), q_stays ? kSoftWarps : 1);
       mbar_init(bar(kBarQEmpty + i), 1);
       mbar_init(bar(kBarSFull + i), 1);
       mbar_init(bar(kBarSEmpty + i), kTeamWarps);
@@ -721,9 +725,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     mbar_init(bar(kBarOFull), 1);
     mbar_init(bar(kBarOEmpty), kSoftWarps);
     mbar_init(bar(kBarDrain), 1);
+    mbar_init(bar(kBarDrain + 1), 1);
     for (int i = 0; i < kOwnWarps * kMaxOwnSlots; ++i) mbar_init(bar(kBarOwn + i), 1);
     for (int i = 0; i < C::kMaxStages; ++i) {
-      mbar_init(bar_kv_full(i), 1);
+      mbar_init(bar_full(0, i), 1);
+      mbar_init(bar_full(1, i), 1);
       mbar_init(bar_kv_empty(i), 1);
     }
     mbar_fence_init();
@@ -982,8 +988,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 #pragma unroll
                 for (int q = 0; q < 8; ++q) psum = __dp4a(pw[q], 0x01010101u, psum);
               }
-              // the set's last P.V has read it
-              if (c == 0 && !mbar_wait_warp(bar(kBarPEmpty + set), ((pi / psets) & 1) ^ 1, kRoleSoftmax)) ok = false;
+              // The set's last P.V has read it.  With one set (F = 4) that was the
+              // other team's: this team's own P.V before it is waited for first,
+              // since a parity says nothing about a phase two ahead of the last one seen.
+              if (c == 0 && ((psets == 1 && pi >= 2 && !mbar_wait_warp(bar(kBarPEmpty), pi & 1, kRoleSoftmax)) ||
+                             !mbar_wait_warp(bar(kBarPEmpty + set), ((pi / psets) & 1) ^ 1, kRoleSoftmax)))
+                ok = false;
               tmem_st8(tlane + kColP + pb * 32 + half * (kCols / 4) + c * 8, pw);
             });
             if (!got) ok = false;
@@ -1071,10 +1081,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     if (static_cast<uint32_t>(lane) < stages) {
       const uint32_t slot = static_cast<uint32_t>(lane);
       const uint32_t dst = sKV + slot * C::kTileBytes;
-      uint32_t n = 0, mine = 0;  // the next load's slot; loads of this lane
+      uint32_t n = 0, mine = 0;       // the next load's slot; loads of this lane
+      uint32_t kinds[2] = {0, 0};     // of them K and V
       bool ok = true;
       // the key tiles of tile j
-      auto load = [&](const CUtensorMap* tm, int j, int hk) {
+      auto load = [&](int v, int j, int hk) {
         const int nf = folds_at(args, j);
         for (int x = 0; x < nf; ++x) {
           const bool other = n != slot;
@@ -1083,9 +1094,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           if (!mbar_wait(bar_kv_empty(slot), (mine & 1) ^ 1, kRoleProducer)) {
             ok = false;
           } else {
-            mbar_arrive_expect_tx(bar_kv_full(slot), C::kTileBytes);
-            tma_load_3d(dst, tm, bar_kv_full(slot), 0, (j * F + x) * kBN, hk);
+            mbar_arrive_expect_tx(bar_full(v, slot), C::kTileBytes);
+            tma_load_3d(dst, v ? &args.tm_v : &args.tm_k, bar_full(v, slot), 0, (j * F + x) * kBN, hk);
             ++mine;
+            kinds[0] += 1 - v;
+            kinds[1] += v;
           }
         }
       };
@@ -1099,43 +1112,49 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
           for (int y = 0; y < turns; ++y) {
             const int j = (y >> 1) - ((y & 1) ? 2 : 0);
             if (j < 0 || j >= sg.n || ((y & 1) && phase < 2)) continue;
-            load((y & 1) ? &args.tm_v : &args.tm_k, sg.j0 + j, sg.hk);
+            load(y & 1, sg.j0 + j, sg.hk);
           }
           t += sg.n;
         }
-      if (mine > 0) mbar_wait(bar_kv_full(slot), (mine - 1) & 1, kRoleProducer);  // no copy left in flight
+      for (int v = 0; v < 2; ++v)  // no copy left in flight
+        if (kinds[v] > 0) mbar_wait(bar_full(v, slot), (kinds[v] - 1) & 1, kRoleProducer);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ============================= MMA issuer =============================
+  } else if (warp == kMmaWarp || warp == kPvWarp) {
+    // ============================= MMA issuers =============================
+    // One warp issues S = Q.K^T, the other O += P.V: an issuing thread moves at
+    // the pace of the tensor pipe and then pays for its waits, so with both
+    // products in one warp the pipe stood still for 40 % of phase C
+    // (B9 H32/8 L50000: @@ us a call against @@).  Both walk the ring's load sequence.
+    const bool pv = warp == kPvWarp;
     const uint32_t idesc_qk = idesc_i8(kBM, kBN, 1, k_u8 ? 0u : 1u, 0);
     const uint32_t idesc_pv = idesc_i8(kBM, D, 0, v_u8 ? 0u : 1u, 1);
     const uint64_t kv_desc0 = smem_desc(sKV, 16, C::kSBO, C::kSwizzle);
     const uint64_t q_desc0 = smem_desc(s_base + C::kOffQ, 16, C::kSBO, C::kSwizzle);
     constexpr uint32_t kSlotDesc = C::kTileBytes >> 4;
     bool ok = true;
-    uint32_t slot = 0, kv_par = 0, sc = 0, pc = 0, nq = 0, no = 0;
+    uint32_t slot = 0, sc = 0, pc = 0, nq = 0, no = 0;
+    uint32_t par = 0;  // bit s: parity of the next phase of slot s's barrier of this warp's kind
     // Waits, all at once: lane 0 for the tile's own barrier, lanes 1 .. nf for
     // the K or V tiles in the next nf ring slots, lane 31 for one more barrier.
     auto wait_tiles = [&](int nf, uint32_t own_bar, uint32_t own_par, uint32_t more_bar, uint32_t more_par) {
-      uint32_t b = own_bar, par = own_par;
+      uint32_t b = own_bar, p = own_par;
       bool mine = lane <= nf;
       if (lane > 0) {
-        const uint32_t s = slot + lane - 1;
-        const bool wraps = s >= stages;
-        b = bar_kv_full(wraps ? s - stages : s);
-        par = kv_par ^ (wraps ? 1u : 0u);
+        const uint32_t s = slot + lane - 1, in = s >= stages ? s - stages : s;
+        b = bar_full(pv ? 1 : 0, in);
+        p = (par >> in) & 1;
       }
       if (lane == 31 && more_bar != 0) {
         b = more_bar;
-        par = more_par;
+        p = more_par;
         mine = true;
       }
-      bool done = !mine || mbar_try_wait(b, par);
+      bool done = !mine || mbar_try_wait(b, p);
       if (__all_sync(0xffffffffu, done)) return true;
       const unsigned long long start = globaltimer_ns();
       while (true) {
-        if (!done) done = mbar_try_wait(b, par);
+        if (!done) done = mbar_try_wait(b, p);
         if (__all_sync(0xffffffffu, done)) return true;
         if (__any_sync(0xffffffffu, globaltimer_ns() - start > kWaitTimeoutNs)) {
           if (lane == 0) atomicOr(&g_device_error, kErrTimeout | (kRoleMma << 8));
@@ -1144,11 +1163,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       }
     };
     auto step = [&](uint32_t s) { return s + 1 == stages ? 0u : s + 1; };
-    auto advance = [&](int nf) {
-      slot += nf;
-      if (slot >= stages) {
-        slot -= stages;
-        kv_par ^= 1;
+    // past nf tiles of the ring, which this warp used or left to the other
+    auto advance = [&](int nf, bool used) {
+      for (int x = 0; x < nf; ++x) {
+        if (used) par ^= 1u << slot;
+        slot = step(slot);
       }
     };
     for (int phase = 0; phase < 3 && ok; ++phase) {
@@ -1156,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       for (int t = t0; t < t1 && ok; ++nq) {
         const Segment sg = segment_at(args, t, t1);
         const uint32_t qb = nq & 1;
-        if (!mbar_wait_warp(bar(kBarQFull + qb), q_stays ? 0u : (nq >> 1) & 1, kRoleMma)) { ok = false; break; }
+        if (!pv && !mbar_wait_warp(bar(kBarQFull + qb), q_stays ? 0u : (nq >> 1) & 1, kRoleMma)) { ok = false; break; }
         const uint64_t q_desc = q_desc0 + ((static_cast<uint32_t>(kBM - RF + kBM * qb) * D) >> 4);
         // S of tile e (the queries in the lanes of fold x against key tile x),
         // then, in phase C, P.V of tile e - 2: S of the next two tiles is
@@ -1165,9 +1184,40 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 #pragma unroll 1
         for (int e = 0; ok && e < turns; ++e) {
           if (e < sg.n) {
-            const uint32_t buf = sc & 1;
             const int nf = folds_at(args, sg.j0 + e);
-            if (!wait_tiles(nf, bar(kBarSEmpty + buf), ((sc >> 1) & 1) ^ 1, 0u, 0u)) {
+            if (!pv) {
+              const uint32_t buf = sc & 1;
+              if (!wait_tiles(nf, bar(kBarSEmpty + buf), ((sc >> 1) & 1) ^ 1, 0u, 0u)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+                uint32_t sl = slot;
+#pragma unroll 1
+                for (int x = 0; x < nf; ++x, sl = step(sl)) {
+                  const uint64_t k_desc = kv_desc0 + sl * kSlotDesc;
+                  const uint64_t a_desc = q_desc - ((static_cast<uint32_t>(x * RF) * D) >> 4);
+#pragma unroll
+                  for (int kk = 0; kk < D / 32; ++kk)
+                    mma_i8_ss(tmem + kColS + buf * kBN, a_desc + 2 * kk, k_desc + 2 * kk, idesc_qk,
+                              (x > 0 || kk > 0) ? 1u : 0u);
+                  mma_commit(bar_kv_empty(sl));
+                }
+                mma_commit(bar(kBarSFull + buf));
+              }
+              __syncwarp();
+              ++sc;
+            }
+            advance(nf, !pv);
+          }
+          const int j = e - 2;
+          if (phase < 2 || j < 0) continue;
+          const int nf = folds_at(args, sg.j0 + j);
+          if (pv) {
+            const uint32_t set = pc & (psets - 1);
+            // the first P.V of a segment: O of the previous one has been read
+            if (!wait_tiles(nf, bar(kBarPFull + set), (pc / psets) & 1, j == 0 ? bar(kBarOEmpty) : 0u, (no & 1) ^ 1)) {
               ok = false;
               break;
             }
@@ -1176,78 +1226,54 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
               uint32_t sl = slot;
 #pragma unroll 1
               for (int x = 0; x < nf; ++x, sl = step(sl)) {
-                const uint64_t k_desc = kv_desc0 + sl * kSlotDesc;
-                const uint64_t a_desc = q_desc - ((static_cast<uint32_t>(x * RF) * D) >> 4);
+                const uint64_t v_desc = kv_desc0 + sl * kSlotDesc;
 #pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk)
-                  mma_i8_ss(tmem + kColS + buf * kBN, a_desc + 2 * kk, k_desc + 2 * kk, idesc_qk, (x > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < kBN / 32; ++kk)
+                  mma_i8_ts(tmem + kColO, tmem + kColP + (set * F + x) * 32 + kk * 8, v_desc + ((32u * D * kk) >> 4),
+                            idesc_pv, (j > 0 || x > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(bar_kv_empty(sl));
               }
-              mma_commit(bar(kBarSFull + buf));
+              mma_commit(bar(kBarPEmpty + set));
+              if (j == sg.n - 1) mma_commit(bar(kBarOFull));
             }
             __syncwarp();
-            advance(nf);
-            ++sc;
+            ++pc;
+            if (j == sg.n - 1) ++no;
           }
-          const int j = e - 2;
-          if (phase < 2 || j < 0) continue;
-          const uint32_t set = pc & (psets - 1);
-          const int nf = folds_at(args, sg.j0 + j);
-          // the first P.V of a segment: O of the previous one has been read
-          if (!wait_tiles(nf, bar(kBarPFull + set), (pc / psets) & 1, j == 0 ? bar(kBarOEmpty) : 0u, (no & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            uint32_t sl = slot;
-#pragma unroll 1
-            for (int x = 0; x < nf; ++x, sl = step(sl)) {
-              const uint64_t v_desc = kv_desc0 + sl * kSlotDesc;
-#pragma unroll
-              for (int kk = 0; kk < kBN / 32; ++kk)
-                mma_i8_ts(tmem + kColO, tmem + kColP + (set * F + x) * 32 + kk * 8, v_desc + ((32u * D * kk) >> 4),
-                          idesc_pv, (j > 0 || x > 0 || kk > 0) ? 1u : 0u);
-              mma_commit(bar_kv_empty(sl));
-            }
-            mma_commit(bar(kBarPEmpty + set));
-            if (j == sg.n - 1) mma_commit(bar(kBarOFull));
-          }
-          __syncwarp();
-          advance(nf);
-          ++pc;
-          if (j == sg.n - 1) ++no;
+          advance(nf, pv);
         }
         if (!ok) break;
-        if (!q_stays) mma_commit_elect(bar(kBarQEmpty + qb));
+        if (!pv && !q_stays) mma_commit_elect(bar(kBarQEmpty + qb));
         t += sg.n;
       }
     }
-    mma_commit_elect(bar(kBarDrain));
-    mbar_wait_warp(bar(kBarDrain), 0, kRoleMma);
+    mma_commit_elect(bar(kBarDrain + (pv ? 1 : 0)));
+    mbar_wait_warp(bar(kBarDrain + (pv ? 1 : 0)), 0, kRoleMma);
   } else {
     // ============================== Q rows ==============================
-    // more than two segments: a half of the rows each, eight loads in flight per lane
+    // more than two segments: eight loads in flight per lane
     if (!q_stays && t0 < t1) {
       constexpr int kBatch = 8;
-      const int qw = warp - kQWarp;
       if (F > 1) {
-        q_zero(qw * 32 + lane, 64);
-        asm volatile("bar.sync 3, 64;" ::: "memory");  // both warps' zeros before the first rows
+        q_zero(lane, 32);
+        __syncwarp();  // before the first rows
       }
       uint32_t nq = 0;
       bool ok = true;
+#pragma unroll 1
       for (int phase = 0; phase < 3 && ok; ++phase)
+#pragma unroll 1
         for (int t = t0; t < t1; ++nq) {
           const Segment sg = segment_at(args, t, t1);
           const uint32_t qb = nq & 1;
           if (!mbar_wait_warp(bar(kBarQEmpty + qb), ((nq >> 1) & 1) ^ 1, kRoleQ)) { ok = false; break; }
-          for (int i0 = 32 * qw; i0 < RF * kPieces; i0 += 64 * kBatch) {
+#pragma unroll 1
+          for (int i0 = 0; i0 < RF * kPieces; i0 += 32 * kBatch) {
             uint4 v[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) v[k] = q_piece(sg, i0 + 64 * k + lane);
+            for (int k = 0; k < kBatch; ++k) v[k] = q_piece(sg, i0 + 32 * k + lane);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) q_store(qb, i0 + 64 * k + lane, v[k]);
+            for (int k = 0; k < kBatch; ++k) q_store(qb, i0 + 32 * k + lane, v[k]);
           }
           fence_proxy_async_smem();
           __syncwarp();

@@ -96,6 +96,11 @@ SWEEP = [  # B, H, Hkv, Lp, Lmax, d
     (40, 8, 2, 640, 130, 128), (64, 2, 2, 511, 5, 128), (65, 2, 1, 200, 9, 64), (70, 6, 2, 385, 40, 128),
     (1, 40, 1, 1500, 700, 128), (2, 9, 3, 0, 1030, 64), (130, 3, 3, 0, 65, 128), (3, 5, 5, 4100, 0, 64),
     (2, 4, 4, 5000, 1100, 128), (9, 32, 2, 130, 20, 64),
+    # few queries over many tiles: four, then two key tiles side by side, the last group partly empty
+    (2, 16, 16, 4900, 30, 64), (3, 32, 32, 2450, 20, 128), (1, 40, 10, 8200, 100, 128),
+    (40, 20, 20, 2100, 17, 64), (7, 64, 8, 5050, 9, 128),
+    # many short tiles: more than two (head, row tile) pairs per CTA
+    (400, 100, 100, 100, 3, 64), (129, 32, 8, 250, 5, 128), (3, 128, 128, 600, 40, 64),
 ]
 
 
