@@ -97,6 +97,7 @@ constexpr int kTeams = 2;                  // softmax teams taking alternate til
 constexpr int kSoftWarps = 16;
 constexpr int kTeamWarps = kSoftWarps / kTeams;
 constexpr int kCols = 64;                  // S columns per thread and tile (two halves)
+constexpr int kChunk = 16;                 // of them read from TMEM at a time
 constexpr int kProducerWarp = 16;
 constexpr int kMmaWarp = 17;               // issues S = Q.K^T
 constexpr int kPvWarp = 18;                // issues O += P.V
@@ -178,6 +179,11 @@ __device__ __forceinline__ int folds_at(const SharedArgs& a, int j) { return min
 
 __device__ __forceinline__ uint32_t bias(int32_t s) { return static_cast<uint32_t>(s) ^ 0x80000000u; }
 __device__ __forceinline__ int32_t unbias(uint32_t u) { return static_cast<int32_t>(u ^ 0x80000000u); }
+
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld32(taddr, v); }
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld16(taddr, v); }
+__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&v)[8]) { tmem_st8(taddr, v); }
+__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&v)[4]) { tmem_st4(taddr, v[0], v[1], v[2], v[3]); }
 
 // Four fp32 adds to consecutive addresses (16-byte aligned).
 __device__ __forceinline__ void red_add4(float* p, float a, float b, float c, float d) {
@@ -842,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       arrive_warp(bar(kBarQFull));
       if (two) arrive_warp(bar(kBarQFull + 1));
     }
-    // The scores of tile `idx`, 32 columns at a time; columns from nv on are
+    // The scores of tile `idx`, kChunk columns at a time; columns from nv on are
     // `low`.  One copy of the body in a rolled loop: the phases' code has to
     // stay small (instruction fetches were a third of the stalls with both
     // halves unrolled and a masked copy beside them).
@@ -851,18 +857,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       if (!mbar_wait_warp(bar(kBarSFull + buf), (idx >> 1) & 1, kRoleSoftmax)) return false;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < kCols / 32; ++c) {
-        uint32_t v[32];
-        tmem_ld32(trow + kColS + buf * kBN + 32 * c, v);
+      for (int c = 0; c < kCols / kChunk; ++c) {
+        uint32_t v[kChunk];
+        ld_cols(trow + kColS + buf * kBN + kChunk * c, v);
         tmem_wait_ld();
-        if (c == kCols / 32 - 1) {
+        if (c == kCols / kChunk - 1) {
           tc_fence_before();
           arrive_warp(bar(kBarSEmpty + buf));
         }
         if (nv < kCols) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (32 * c + k >= nv) v[k] = low;
+          for (int k = 0; k < kChunk; ++k)
+            if (kChunk * c + k >= nv) v[k] = low;
         }
         body(v, c);
       }
@@ -880,9 +886,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
       int32_t m = INT_MIN;
       for (int j = first_j(sc); j < sg.n; j += kTeams) {
         int32_t m4[4] = {INT_MIN, INT_MIN, INT_MIN, INT_MIN};
-        const bool got = walk_s(sc + j, nvalid(sg.j0 + j), 0x80000000u, [&](const uint32_t (&v)[32], int) {
+        const bool got = walk_s(sc + j, nvalid(sg.j0 + j), 0x80000000u, [&](const uint32_t (&v)[kChunk], int) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
+          for (int k = 0; k < kChunk; k += 8) {
             m4[0] = __vimax3_s32(m4[0], static_cast<int32_t>(v[k + 0]), static_cast<int32_t>(v[k + 1]));
             m4[1] = __vimax3_s32(m4[1], static_cast<int32_t>(v[k + 2]), static_cast<int32_t>(v[k + 3]));
             m4[2] = __vimax3_s32(m4[2], static_cast<int32_t>(v[k + 4]), static_cast<int32_t>(v[k + 5]));
@@ -937,9 +943,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         int32_t Z = 0;
         for (int j = first_j(sc); j < sg.n; j += kTeams) {
           int32_t z4[4] = {0, 0, 0, 0};
-          const bool got = walk_s(sc + j, nvalid(sg.j0 + j), masked(), [&](const uint32_t (&v)[32], int) {
+          const bool got = walk_s(sc + j, nvalid(sg.j0 + j), masked(), [&](const uint32_t (&v)[kChunk], int) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
+            for (int k = 0; k < kChunk; k += 2) {
               uint32_t b0, b1;
               idx_bits2(v[k], v[k + 1], b0, b1);
               z4[k & 3] += static_cast<int32_t>(lds_u32(b0 * 512u + prow));
@@ -973,10 +979,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
             const uint32_t pi = pc + j;
             const uint32_t set = pi & (psets - 1);
             const uint32_t pb = set * F + f;  // this fold's buffer of the set
-            const bool got = walk_s(sc + j, nvalid(sg.j0 + j), masked(), [&](const uint32_t (&v)[32], int c) {
-              uint32_t pw[8];
+            const bool got = walk_s(sc + j, nvalid(sg.j0 + j), masked(), [&](const uint32_t (&v)[kChunk], int c) {
+              uint32_t pw[kChunk / 4];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
+              for (int q = 0; q < kChunk / 4; ++q) {
                 uint32_t kb[4], p[4];
                 idx_bits2(v[q * 4], v[q * 4 + 1], kb[0], kb[1]);
                 idx_bits2(v[q * 4 + 2], v[q * 4 + 3], kb[2], kb[3]);
@@ -986,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
               }
               if (v_u8) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) psum = __dp4a(pw[q], 0x01010101u, psum);
+                for (int q = 0; q < kChunk / 4; ++q) psum = __dp4a(pw[q], 0x01010101u, psum);
               }
               // The set's last P.V has read it.  With one set (F = 4) that was the
               // other team's: this team's own P.V before it is waited for first,
@@ -994,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
               if (c == 0 && ((psets == 1 && pi >= 2 && !mbar_wait_warp(bar(kBarPEmpty), pi & 1, kRoleSoftmax)) ||
                              !mbar_wait_warp(bar(kBarPEmpty + set), ((pi / psets) & 1) ^ 1, kRoleSoftmax)))
                 ok = false;
-              tmem_st8(tlane + kColP + pb * 32 + half * (kCols / 4) + c * 8, pw);
+              st_cols(tlane + kColP + pb * 32 + half * (kCols / 4) + c * (kChunk / 4), pw);
             });
             if (!got) ok = false;
             if (!ok) break;
