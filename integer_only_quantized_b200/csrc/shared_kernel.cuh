@@ -221,7 +221,7 @@ __device__ __forceinline__ int own_rows(const SharedArgs& a, int b) {
 // The blocks of `keys` own rows of every sequence and unit (K / V head, group
 // of eight query heads), in the order (b, unit, block), and a warp's
 // place among them.  Warp-collective.
-constexpr int kUnitCost = 1;  // blocks' worth of work in changing the unit, for equal shares
+constexpr int kUnitCost = 2;  // blocks' worth of work in changing the unit, for equal shares
 struct Walk {
   int b, hk, g, blk, nb;  // sequence, K / V head, group of eight query heads; nb: blocks of the sequence
   // the share of warp `w` of `warps`: its first block (where there is one), and their number
