@@ -406,11 +406,11 @@ typedef struct intattn_rows {
  *             (a, b) -> (a c - b s, a s + b c), (c, s) = table[p][f].
  *             table: DEVICE fp32 [n_positions, rot/2, 2], 16-byte aligned
  *             (NULL: no rotation); rot a multiple of 16, <= d; positions:
- *             DEVICE int32 [B, L].  A row whose position is negative is
- *             padding: it is neither read nor written.  A position >=
+ *             DEVICE int32 [B, L] (NULL without a table).  A row whose position is negative is
+ *             padding: its values do not matter and it is not written.  A position >=
  *             n_positions leaves its rows unwritten and is reported by
  *             intattn_device_error (INTATTN_ERR_PARAM_RANGE).
- * All of it in fp32. */
+ * All of it in fp32 (a mean square past its range, |x| above 10^18, gives 0). */
 typedef struct intattn_rope_norm {
     const float *w_q, *w_k;
     float eps;               /* finite, > 0 */

@@ -82,6 +82,14 @@ def _host_array(x, dtype) -> np.ndarray:
     return np.ascontiguousarray(np.atleast_1d(np.asarray(x)).astype(dtype, copy=False))
 
 
+def _address(a: np.ndarray) -> int:
+    """Address of a's data (through the buffer where it is writable, the fastest way)."""
+    try:
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))
+    except (TypeError, ValueError):  # read-only or empty
+        return a.ctypes.data
+
+
 @dataclasses.dataclass
 class Scales:
     """Quantisation scales (real = scale * code).  per_head: arrays of H.
@@ -102,14 +110,14 @@ class Scales:
         f32 = np.float32
         arrs = [_host_array(self.s_q, f32), _host_array(self.s_k, f32), _host_array(self.s_v, f32),
                 _host_array(self.s_o, f32)]
-        s = _Scales(int(bool(self.per_head)), *[a.__array_interface__["data"][0] for a in arrs])
+        s = _Scales(int(bool(self.per_head)), *[_address(a) for a in arrs])
         if self.clip is not None:
             arrs.append(_host_array(self.clip, f32))
-            s.clip_c = arrs[-1].__array_interface__["data"][0]
+            s.clip_c = _address(arrs[-1])
         for name, z in (("z_k", self.z_k), ("z_v", self.z_v)):
             if z is not None:
                 arrs.append(_host_array(z, np.int32))
-                setattr(s, name, arrs[-1].__array_interface__["data"][0])
+                setattr(s, name, _address(arrs[-1]))
         return s, arrs  # keep the arrays alive for the duration of the call
 
 
@@ -506,6 +514,8 @@ class _On:
 
     def __enter__(self) -> int:
         import torch
+        if getattr(self.stream, "device", self.device) != self.device:
+            raise ValueError(f"stream is on {self.stream.device}, the tensors are on {self.device}")
         self.guards.append(torch.cuda.device(self.device))
         self.guards[0].__enter__()
         s = self.stream
@@ -606,7 +616,8 @@ class RopeNorm:
 
     def _c(self, B: int, L: int, d: int, device) -> _RopeNorm:
         import torch
-        c = _RopeNorm(eps=float(self.eps), interleaved=int(bool(self.interleaved)))
+        c = _RopeNorm()
+        c.eps, c.interleaved = self.eps, bool(self.interleaved)
         for name in ("w_q", "w_k"):
             w = getattr(self, name)
             if w is not None:
@@ -619,10 +630,12 @@ class RopeNorm:
             t = self.table
             if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device:
                 raise TypeError(f"table must be a float32 tensor on {device}")
-            if t.dim() != 3 or t.shape[2] != 2 or not t.is_contiguous():
-                raise ValueError("table must be contiguous [n_positions, rot / 2, 2]")
+            if t.dim() != 3 or t.shape[2] != 2 or t.numel() == 0 or not t.is_contiguous():
+                raise ValueError("table must be contiguous [n_positions, rot / 2, 2] and not empty")
             c.table, c.n_positions, c.rot = t.data_ptr(), t.shape[0], 2 * t.shape[1]
             c.positions = _index_tensor(self.positions, "positions", (B, L), device)
+        elif self.positions is not None:
+            raise ValueError("positions without a table")
         return c
 
 
@@ -635,6 +648,18 @@ def rope_table(n_positions: int, rot: int, base: float = 10000.0, device="cuda")
     f = float(base) ** (-torch.arange(0, rot, 2, device=device, dtype=torch.float64) / rot)
     a = torch.arange(n_positions, device=device, dtype=torch.float64)[:, None] * f
     return torch.stack([a.cos(), a.sin()], dim=-1).float().contiguous()
+
+
+def _rows_out(t, name: str, like):
+    """An output of the shape and type of `like` (None: a new one) and its _Rows."""
+    if t is None:
+        B, h, L, d = like.shape
+        t = like.new_empty((B, h, L, d))
+        return t, _Rows(t.data_ptr(), h * L * d, L * d, d)
+    r = _rows(t, name, like.device, like.dtype)
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must be {list(like.shape)}")
+    return t, r
 
 
 def qk_norm_rope(q, k, norm: RopeNorm, q_out=None, k_out=None, stream=None):
@@ -658,15 +683,9 @@ def qk_norm_rope(q, k, norm: RopeNorm, q_out=None, k_out=None, stream=None):
         raise ValueError("k_out without k")
     c = norm._c(B, L, d, dev)
     with _on(dev, stream) as st:
-        if q_out is None:
-            q_out = torch.empty((B, H, L, d), dtype=dt, device=dev)
-        if k is not None and k_out is None:
-            k_out = torch.empty((B, Hkv, L, d), dtype=dt, device=dev)
-        qor = _rows(q_out, "q_out", dev, dt)
+        q_out, qor = _rows_out(q_out, "q_out", q)
         if k is not None:
-            kor = _rows(k_out, "k_out", dev, dt)
-        if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-            raise ValueError("outputs must match q and k")
+            k_out, kor = _rows_out(k_out, "k_out", k)
         _check(lib().intattn_qk_norm_rope(qr, kr, c, _row_types()[dt], B, H, Hkv, L, d, qor, kor, st), "intattn_qk_norm_rope")
     return q_out, k_out
 
@@ -721,7 +740,7 @@ def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bit
     with _on(dev, stream) as st:
         if q is not None:
             if q_out is None:
-                q_out = torch.empty((B, H, L, d), dtype=torch.int8, device=dev)
+                q_out = q.new_empty((B, H, L, d), dtype=torch.int8)
             _check_tensor(q_out, "q_out")
             if q_out.shape != q.shape or q_out.device != dev:
                 raise ValueError("q_out must match q")
@@ -764,9 +783,9 @@ def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bi
     sc, keep = scales._c()
     with _on(dev, stream) as st:
         if k_out is None:
-            k_out = torch.empty((B, Hkv, L, d), dtype=dt, device=dev)
+            k_out = k_cache.new_empty((B, Hkv, L, d), dtype=dt)
         if v_out is None and v_cache is not None:
-            v_out = torch.empty((B, Hkv, L, d), dtype=dt, device=dev)
+            v_out = k_cache.new_empty((B, Hkv, L, d), dtype=dt)
         for t, n in ((k_out, "k_out"), (v_out, "v_out")):
             if t is None:
                 continue
@@ -825,13 +844,15 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lengths, scales: Scal
     sc, keep = scales._c()
     with _on(dev, stream) as st:
         if out is None:
-            out = torch.empty((B, H, 1, d), dtype=dt, device=dev)
+            out = q.new_empty((B, H, 1, d), dtype=dt)
         if not isinstance(out, torch.Tensor) or out.dtype != dt or out.device != dev:
             raise TypeError(f"out must be a {dt} tensor on {dev}")
         if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous and match q")
         if workspace is None:
-            workspace = torch.empty(max(decode_shared_workspace_size(B, H, Hkv, Lmax, d), 1), dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(decode_shared_workspace_size(B, H, Hkv, Lmax, d), dtype=torch.uint8)
+        elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         rc = lib().intattn_decode_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), Lp, Lp_max,
                                          k_cache.data_ptr(), v_cache.data_ptr(), lp, sc, B, H, Hkv, Lmax, d,
                                          float(clip_c), kinds[dt], out.data_ptr(), workspace.data_ptr(),

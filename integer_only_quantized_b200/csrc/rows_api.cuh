@@ -6,6 +6,7 @@ namespace {
 
 using intattn::ReadArgs;
 using intattn::RowArgs;
+using intattn::RowCodeArgs;
 using intattn::RowTensor;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -21,6 +22,7 @@ int check_rows(const intattn_rows_t* r, int B, int heads, int L, bool output) {
 }
 
 int check_rope_norm(const intattn_rope_norm_t* rn, int d, RowArgs* a) {
+  if (rn->positions && !rn->table) return INTATTN_ERR_INVALID_ARG;
   if (rn->table) {
     if (!rn->positions || rn->n_positions < 1 || rn->rot < 0 || rn->rot > d) return INTATTN_ERR_INVALID_ARG;
     if (rn->rot % 16 || !aligned16(rn->table) || !aligned4(rn->positions)) return INTATTN_ERR_UNSUPPORTED;
@@ -50,7 +52,7 @@ void set_input(RowTensor* t, const intattn_rows_t* r, int heads) {
 // flight (D / 8 lanes and four loads per lane) when that still gives every SM
 // several warps, else one load's worth, so that few tokens spread over more SMs.
 template <bool kCodes>
-int rows_launch(RowArgs& a, int d, cudaStream_t st) {
+int rows_launch(intattn::RowCall<kCodes>& a, int d, cudaStream_t st) {
   int sms = 0;
   if (sm_count(&sms) != INTATTN_OK) return INTATTN_ERR_CUDA;
   const int per_load = 256 / d;
@@ -104,7 +106,6 @@ int intattn_qk_norm_rope(const intattn_rows_t* q, const intattn_rows_t* k, const
   if (d != 64 && d != 128) return INTATTN_ERR_UNSUPPORTED;
   if (dtype != INTATTN_DTYPE_FP16 && dtype != INTATTN_DTYPE_BF16) return INTATTN_ERR_UNSUPPORTED;
   if (H > 65535 || Hkv > 65535) return INTATTN_ERR_UNSUPPORTED;
-  static_assert(sizeof(RowArgs) <= 8192, "kernel argument block too large");
   RowArgs a;
   std::memset(&a, 0, sizeof(a));
   int rc = check_rope_norm(rn, d, &a);
@@ -141,7 +142,8 @@ int intattn_cache_write(const intattn_rows_t* k, const intattn_rows_t* v, const 
   if (bits != 8 && bits != 4) return INTATTN_ERR_UNSUPPORTED;
   if (Hkv > 65535 || (q && H > 65535)) return INTATTN_ERR_UNSUPPORTED;
   if (scales->per_head && (Hkv > INTATTN_MAX_HEADS || (q && H > INTATTN_MAX_HEADS))) return INTATTN_ERR_UNSUPPORTED;
-  RowArgs a;
+  static_assert(sizeof(RowCodeArgs) <= 8192, "kernel argument block too large");
+  RowCodeArgs a;
   std::memset(&a, 0, sizeof(a));
   int rc;
   if (rn && (rc = check_rope_norm(rn, d, &a))) return rc;
@@ -226,7 +228,7 @@ int intattn_cache_read(const void* k_cache, const void* v_cache, const intattn_s
   a.start = start;
   a.lengths = lengths;
   const int per_cta = intattn::rows::kReadThreads / (d / 8) * intattn::rows::kReadUnroll;
-  a.chunks = (L + per_cta - 1) / per_cta;
+  a.chunks = (L - 1) / per_cta + 1;
   const long long grid = static_cast<long long>(a.chunks) * B * Hkv * a.n_tensors;
   if (grid > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -57,9 +57,15 @@ struct RowArgs {
   const float2* table;         // [n_positions, rot / 2] (cos, sin)
   int32_t n_positions, rot, interleaved;
   float eps;
-  float inv[3 * INTATTN_MAX_HEADS];    // codes: RN32(1 / scale)
+};
+// with codes: 6 KB more, which a call without them need not hand over
+struct RowCodeArgs : RowArgs {
+  float inv[3 * INTATTN_MAX_HEADS];    // RN32(1 / scale)
   float zero[3 * INTATTN_MAX_HEADS];   // zero-points (0: symmetric)
 };
+template <bool kCodes> struct RowCallOf { using type = RowArgs; };
+template <> struct RowCallOf<true> { using type = RowCodeArgs; };
+template <bool kCodes> using RowCall = typename RowCallOf<kCodes>::type;
 
 struct ReadArgs {
   const uint8_t* in[2];   // caches [B, H, Lmax, d] (4 bits: d / 2 bytes a row)
@@ -155,7 +161,7 @@ __device__ __forceinline__ void codes4(const float2 (&y)[2], float inv, float lo
 
 // kCodes: the output is codes; else fp16 / bf16.
 template <int D, bool kCodes, bool kBf16>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowCall<kCodes> a) {
   constexpr int kLpr = D / 8;           // lanes per row
   constexpr int kRpw = 32 / kLpr;       // rows (heads) per warp and load
   constexpr int kUnroll = 4;            // loads in flight per lane

@@ -35,8 +35,8 @@ def _close(got, want, mag, dtype):
     """One rounding to dtype (half a step relative, half the smallest
     subnormal) of an fp32 value.  fp32 part, in units of 2^-24 of the magnitudes
     added: the sum of up to 128 squares (8 fused steps, 4 shuffled adds: 12,
-    halved by the root: 6), mean and eps 2 (halved: 1), root 1, quotient 1, two products 2,
-    rotation 3; 16 covers them."""
+    halved by the root: 6), mean and eps 2 (halved: 1), reciprocal root 4 (two units
+    in the last place), two products 2, rotation 3: 16."""
     import torch
     eps = torch.finfo(dtype).eps
     tiny = torch.finfo(dtype).smallest_normal * eps
@@ -353,3 +353,40 @@ def test_python_refusals(ia):
     with pytest.raises(ValueError):
         ia.cache_read(c, None, sc, st, 3, v_out=x)
     assert ia.device_error() == ia.OK
+
+
+def test_more_python_refusals(ia):
+    """Tables and positions that would rotate nothing, and a stream of another device."""
+    import torch
+    x = torch.zeros((1, 2, 3, 64), dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros((1, 3), dtype=torch.int32, device="cuda")
+
+    class Elsewhere:
+        cuda_stream, device = 0, torch.device("cuda", torch.cuda.current_device() + 1)
+
+    table = ia.rope_table(4, 64)
+    for rn in (ia.RopeNorm(None, pos), ia.RopeNorm(table[:0], pos), ia.RopeNorm(table[:, :0].contiguous(), pos)):
+        with pytest.raises(ValueError):
+            ia.qk_norm_rope(x, None, rn)
+    with pytest.raises(ValueError):
+        ia.qk_norm_rope(x, x, ia.RopeNorm(table, pos), k_out=x[:, :1])
+    with pytest.raises(ValueError):
+        ia.qk_norm_rope(x, None, ia.RopeNorm(table, pos), stream=Elsewhere())
+    assert ia.device_error() == ia.OK
+
+
+def test_scales_from_read_only_arrays(ia):
+    """Scale arrays that cannot be written give the codes of those that can."""
+    import torch
+    rng = np.random.default_rng(31)
+    k = torch.from_numpy(rng.standard_normal((1, 4, 5, 64)).astype(np.float32)).cuda().bfloat16()
+    s = np.array([0.02, 0.03, 0.01, 0.05], np.float32)
+    frozen = s.copy()
+    frozen.flags.writeable = False
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = []
+    for x in (s, frozen, s.tolist()):
+        kc, vc = (torch.zeros((1, 4, 8, 64), dtype=torch.int8, device="cuda") for _ in range(2))
+        ia.cache_write(k, k, ia.Scales(1, x, x, 1, per_head=True), kc, vc, st)
+        out.append(torch.cat([kc, vc]))
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2]) and bool(out[0].any())

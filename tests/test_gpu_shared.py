@@ -363,3 +363,24 @@ def test_python_refusals(ia):
                     (ia.IntAttnError, dict(workspace=torch.empty(4, dtype=torch.uint8, device="cuda")))]:
         with pytest.raises(err):
             ia.decode_shared(**{**f, **kw})
+
+
+def test_workspace_of_another_place(ia):
+    """A workspace that is not a contiguous tensor of the call's device."""
+    import torch
+    c = Case(2, 4, 2, 70, 20, 64, 77)
+    q, kp, vp, kc, vc, ln = c.dev()
+    n = ia.decode_shared_workspace_size(2, 4, 2, 20, 64)
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty((n, 2), dtype=torch.uint8, device="cuda")[:, 0], n):
+        with pytest.raises(ValueError):
+            ia.decode_shared(q, kp, vp, kc, vc, ln, c.scales(ia), c.clip, workspace=ws)
+
+
+def test_output_over_the_queries(ia, oracle_mod):
+    """out = q: the queries are read before any output is written, with many
+    row tiles and segments too."""
+    for shape in ((2, 4, 2, 700, 40, 64), (40, 16, 2, 1500, 30, 128)):
+        c = Case(*shape, 78)
+        q, kp, vp, kc, vc, ln = c.dev()
+        ia.decode_shared(q, kp, vp, kc, vc, ln, c.scales(ia), c.clip, out=q)
+        _equal(q, c.want(oracle_mod))

@@ -156,3 +156,8 @@ def test_oracle_codes_by_hand():
     assert orow.codes(x, [0.5], [7], 4).ravel().tolist() == [7, 9, 7, 5, 15, 15, 0, 15, 0, 7, 8, 7]
     c = np.arange(-7, 8).repeat(2)[:16]
     assert np.array_equal(orow.unpack(orow.pack(c, 4, False), 4, False), c)
+
+
+def test_positions_without_a_table_are_refused(ia):
+    assert _norm(ia, table=None) == ia.ERR_INVALID_ARG
+    assert _norm(ia, table=None, positions=None, B=0) == ia.OK
