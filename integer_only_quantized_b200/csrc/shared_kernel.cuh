@@ -1128,133 +1128,118 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ============================= MMA issuers =============================
-    // One warp issues S = Q.K^T, the other O += P.V: an issuing thread moves at
-    // the pace of the tensor pipe and then pays for its waits, so with both
-    // products in one warp the pipe stood still for 40 % of phase C
-    // (B9 H32/8 L50000: @@ us a call against @@).  Both walk the ring's load sequence.
-    const bool pv = warp == kPvWarp;
-    const uint32_t idesc_qk = idesc_i8(kBM, kBN, 1, k_u8 ? 0u : 1u, 0);
-    const uint32_t idesc_pv = idesc_i8(kBM, D, 0, v_u8 ? 0u : 1u, 1);
-    const uint64_t kv_desc0 = smem_desc(sKV, 16, C::kSBO, C::kSwizzle);
-    const uint64_t q_desc0 = smem_desc(s_base + C::kOffQ, 16, C::kSBO, C::kSwizzle);
-    constexpr uint32_t kSlotDesc = C::kTileBytes >> 4;
-    bool ok = true;
-    uint32_t slot = 0, sc = 0, pc = 0, nq = 0, no = 0;
-    uint32_t par = 0;  // bit s: parity of the next phase of slot s's barrier of this warp's kind
-    // Waits, all at once: lane 0 for the tile's own barrier, lanes 1 .. nf for
-    // the K or V tiles in the next nf ring slots, lane 31 for one more barrier.
-    auto wait_tiles = [&](int nf, uint32_t own_bar, uint32_t own_par, uint32_t more_bar, uint32_t more_par) {
-      uint32_t b = own_bar, p = own_par;
-      bool mine = lane <= nf;
-      if (lane > 0) {
-        const uint32_t s = slot + lane - 1, in = s >= stages ? s - stages : s;
-        b = bar_full(pv ? 1 : 0, in);
-        p = (par >> in) & 1;
-      }
-      if (lane == 31 && more_bar != 0) {
-        b = more_bar;
-        p = more_par;
-        mine = true;
-      }
-      bool done = !mine || mbar_try_wait(b, p);
-      if (__all_sync(0xffffffffu, done)) return true;
-      const unsigned long long start = globaltimer_ns();
-      while (true) {
-        if (!done) done = mbar_try_wait(b, p);
-        if (__all_sync(0xffffffffu, done)) return true;
-        if (__any_sync(0xffffffffu, globaltimer_ns() - start > kWaitTimeoutNs)) {
-          if (lane == 0) atomicOr(&g_device_error, kErrTimeout | (kRoleMma << 8));
-          return false;
-        }
-      }
-    };
-    auto step = [&](uint32_t s) { return s + 1 == stages ? 0u : s + 1; };
-    // past nf tiles of the ring, which this warp used or left to the other
-    auto advance = [&](int nf, bool used) {
-      for (int x = 0; x < nf; ++x) {
-        if (used) par ^= 1u << slot;
-        slot = step(slot);
-      }
-    };
-    for (int phase = 0; phase < 3 && ok; ++phase) {
-      if (q_stays) nq = 0;
-      for (int t = t0; t < t1 && ok; ++nq) {
-        const Segment sg = segment_at(args, t, t1);
-        const uint32_t qb = nq & 1;
-        if (!pv && !mbar_wait_warp(bar(kBarQFull + qb), q_stays ? 0u : (nq >> 1) & 1, kRoleMma)) { ok = false; break; }
-        const uint64_t q_desc = q_desc0 + ((static_cast<uint32_t>(kBM - RF + kBM * qb) * D) >> 4);
-        // S of tile e (the queries in the lanes of fold x against key tile x),
-        // then, in phase C, P.V of tile e - 2: S of the next two tiles is
-        // always issued before the P.V that waits for the softmax
-        const int turns = sg.n + (phase == 2 ? 2 : 0);
+    // One thread issues S = Q.K^T, another O += P.V.  Both walk the ring's load
+    // sequence (K of tile e, then in phase C V of tile e - 2), each past the
+    // other's slots.  What lies between two tiles' products is the latency of a few
+    // dependent instructions, in which the tensor pipe stands still: so one
+    // thread runs the whole loop, and waits for a K or V tile only before its
+    // own products, while those of the one before it run.
+    if (elect_one()) {
+      const bool pv = warp == kPvWarp;
+      const uint64_t kv_desc0 = smem_desc(sKV, 16, C::kSBO, C::kSwizzle);
+      constexpr uint32_t kSlotDesc = C::kTileBytes >> 4;
+      bool ok = true;
+      uint32_t slot = 0;
+      uint32_t par = 0;  // bit s: parity of the next phase of slot s's barrier of this warp's kind
+      auto past = [&](uint32_t n) {  // n slots on (n <= 2 F, F <= stages)
+        slot += n;
+        if (slot >= stages) slot -= stages;
+      };
+      // the K or V tile in the next slot; with its products issued, `taken` moves on
+      auto arrived = [&]() { return mbar_wait(bar_full(pv ? 1 : 0, slot), (par >> slot) & 1, kRoleMma); };
+      auto taken = [&]() {
+        mma_commit(bar_kv_empty(slot));
+        par ^= 1u << slot;
+        past(1);
+      };
+      if (!pv) {
+        const uint32_t idesc = idesc_i8(kBM, kBN, 1, k_u8 ? 0u : 1u, 0);
+        const uint64_t q_desc0 = smem_desc(s_base + C::kOffQ, 16, C::kSBO, C::kSwizzle);
+        uint32_t sc = 0, nq = 0;
+        for (int phase = 0; phase < 3 && ok; ++phase) {
+          if (q_stays) nq = 0;
+          for (int t = t0; t < t1 && ok; ++nq) {
+            const Segment sg = segment_at(args, t, t1);
+            const uint32_t qb = nq & 1;
+            if (!mbar_wait(bar(kBarQFull + qb), q_stays ? 0u : (nq >> 1) & 1, kRoleMma)) { ok = false; break; }
+            const uint64_t q_desc = q_desc0 + ((static_cast<uint32_t>(kBM - RF + kBM * qb) * D) >> 4);
 #pragma unroll 1
-        for (int e = 0; ok && e < turns; ++e) {
-          if (e < sg.n) {
-            const int nf = folds_at(args, sg.j0 + e);
-            if (!pv) {
+            for (int e = 0; e < sg.n; ++e) {
+              const int nf = folds_at(args, sg.j0 + e);
               const uint32_t buf = sc & 1;
-              if (!wait_tiles(nf, bar(kBarSEmpty + buf), ((sc >> 1) & 1) ^ 1, 0u, 0u)) {
-                ok = false;
-                break;
-              }
+              if (!(ok = mbar_wait(bar(kBarSEmpty + buf), ((sc >> 1) & 1) ^ 1, kRoleMma))) break;
               tc_fence_after();
-              if (elect_one()) {
-                uint32_t sl = slot;
+              // the queries in the lanes of fold x against key tile x
 #pragma unroll 1
-                for (int x = 0; x < nf; ++x, sl = step(sl)) {
-                  const uint64_t k_desc = kv_desc0 + sl * kSlotDesc;
-                  const uint64_t a_desc = q_desc - ((static_cast<uint32_t>(x * RF) * D) >> 4);
+              for (int x = 0; x < nf; ++x) {
+                if (!(ok = arrived())) break;
+                const uint64_t k_desc = kv_desc0 + slot * kSlotDesc;
+                const uint64_t a_desc = q_desc - ((static_cast<uint32_t>(x * RF) * D) >> 4);
 #pragma unroll
-                  for (int kk = 0; kk < D / 32; ++kk)
-                    mma_i8_ss(tmem + kColS + buf * kBN, a_desc + 2 * kk, k_desc + 2 * kk, idesc_qk,
-                              (x > 0 || kk > 0) ? 1u : 0u);
-                  mma_commit(bar_kv_empty(sl));
-                }
-                mma_commit(bar(kBarSFull + buf));
+                for (int kk = 0; kk < D / 32; ++kk)
+                  mma_i8_ss(tmem + kColS + buf * kBN, a_desc + 2 * kk, k_desc + 2 * kk, idesc, (x > 0 || kk > 0) ? 1u : 0u);
+                taken();
               }
-              __syncwarp();
+              if (!ok) break;
+              mma_commit(bar(kBarSFull + buf));
               ++sc;
+              if (phase == 2 && e >= 2) past(F);  // V of tile e - 2, not the head's last: a full one
             }
-            advance(nf, !pv);
+            // V of the segment's last two tiles
+            if (phase == 2)
+              for (int e = max(sg.n - 2, 0); e < sg.n; ++e) past(folds_at(args, sg.j0 + e));
+            if (!ok) break;
+            if (!q_stays) mma_commit(bar(kBarQEmpty + qb));
+            t += sg.n;
           }
-          const int j = e - 2;
-          if (phase < 2 || j < 0) continue;
-          const int nf = folds_at(args, sg.j0 + j);
-          if (pv) {
+        }
+      } else {
+        const uint32_t idesc = idesc_i8(kBM, D, 0, v_u8 ? 0u : 1u, 1);
+        const int set_bits = F == 1 ? 2 : F == 2 ? 1 : 0;  // of the P sets
+        uint32_t pc = 0, no = 0;
+        // K tiles of phases A and B
+        uint32_t before = 0;
+        for (int t = t0; t < t1;) {
+          const Segment sg = segment_at(args, t, t1);
+          before += 2 * (min((sg.j0 + sg.n) * F, args.key_tiles) - sg.j0 * F);
+          t += sg.n;
+        }
+        slot = before % stages;
+        for (int t = t0; t < t1 && ok; ++no) {
+          const Segment sg = segment_at(args, t, t1);
+          for (int e = 0; e < min(sg.n, 2); ++e) past(folds_at(args, sg.j0 + e));  // K of the first two tiles
+#pragma unroll 1
+          for (int j = 0; j < sg.n; ++j) {
+            if (j + 2 < sg.n) past(folds_at(args, sg.j0 + j + 2));
+            const int nf = folds_at(args, sg.j0 + j);
             const uint32_t set = pc & (psets - 1);
             // the first P.V of a segment: O of the previous one has been read
-            if (!wait_tiles(nf, bar(kBarPFull + set), (pc / psets) & 1, j == 0 ? bar(kBarOEmpty) : 0u, (no & 1) ^ 1)) {
-              ok = false;
-              break;
-            }
+            ok = (j > 0 || mbar_wait(bar(kBarOEmpty), (no & 1) ^ 1, kRoleMma)) &&
+                 mbar_wait(bar(kBarPFull + set), (pc >> set_bits) & 1, kRoleMma);
+            if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-              uint32_t sl = slot;
 #pragma unroll 1
-              for (int x = 0; x < nf; ++x, sl = step(sl)) {
-                const uint64_t v_desc = kv_desc0 + sl * kSlotDesc;
+            for (int x = 0; x < nf; ++x) {
+              if (!(ok = arrived())) break;
+              const uint64_t v_desc = kv_desc0 + slot * kSlotDesc;
 #pragma unroll
-                for (int kk = 0; kk < kBN / 32; ++kk)
-                  mma_i8_ts(tmem + kColO, tmem + kColP + (set * F + x) * 32 + kk * 8, v_desc + ((32u * D * kk) >> 4),
-                            idesc_pv, (j > 0 || x > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(bar_kv_empty(sl));
-              }
-              mma_commit(bar(kBarPEmpty + set));
-              if (j == sg.n - 1) mma_commit(bar(kBarOFull));
+              for (int kk = 0; kk < kBN / 32; ++kk)
+                mma_i8_ts(tmem + kColO, tmem + kColP + (set * F + x) * 32 + kk * 8, v_desc + ((32u * D * kk) >> 4), idesc,
+                          (j > 0 || x > 0 || kk > 0) ? 1u : 0u);
+              taken();
             }
-            __syncwarp();
+            if (!ok) break;
+            mma_commit(bar(kBarPEmpty + set));
+            if (j == sg.n - 1) mma_commit(bar(kBarOFull));
             ++pc;
-            if (j == sg.n - 1) ++no;
           }
-          advance(nf, pv);
+          t += sg.n;
         }
-        if (!ok) break;
-        if (!pv && !q_stays) mma_commit_elect(bar(kBarQEmpty + qb));
-        t += sg.n;
       }
+      mma_commit(bar(kBarDrain + (pv ? 1 : 0)));
+      mbar_wait(bar(kBarDrain + (pv ? 1 : 0)), 0, kRoleMma);
     }
-    mma_commit_elect(bar(kBarDrain + (pv ? 1 : 0)));
-    mbar_wait_warp(bar(kBarDrain + (pv ? 1 : 0)), 0, kRoleMma);
+    __syncwarp();
   } else {
     // ============================== Q rows ==============================
     // more than two segments: eight loads in flight per lane
