@@ -73,13 +73,16 @@ class _RopeNorm(ctypes.Structure):
 FloatArg = Union[float, Sequence[float], np.ndarray]
 
 
+_F32, _I32 = np.dtype(np.float32), np.dtype(np.int32)
+
+
 def _host_array(x, dtype) -> np.ndarray:
-    """x as a contiguous 1-D host array (x itself where it is one)."""
-    if type(x) is np.ndarray and x.dtype == dtype and x.ndim == 1 and x.flags.c_contiguous:
+    """x as a contiguous host array of at least one dimension (x itself where it is one)."""
+    if type(x) is np.ndarray and x.dtype is dtype and x.ndim == 1 and x.flags.c_contiguous:
         return x
     if type(x) is float or type(x) is int:
         return np.array((x,), dtype)
-    return np.ascontiguousarray(np.atleast_1d(np.asarray(x)).astype(dtype, copy=False))
+    return np.array(x, dtype, ndmin=1, order="C")
 
 
 def _address(a: np.ndarray) -> int:
@@ -106,19 +109,27 @@ class Scales:
     z_k: Optional[FloatArg] = None
     z_v: Optional[FloatArg] = None
 
-    def _c(self):
-        f32 = np.float32
-        arrs = [_host_array(self.s_q, f32), _host_array(self.s_k, f32), _host_array(self.s_v, f32),
-                _host_array(self.s_o, f32)]
-        s = _Scales(int(bool(self.per_head)), *[_address(a) for a in arrs])
-        if self.clip is not None:
-            arrs.append(_host_array(self.clip, f32))
-            s.clip_c = _address(arrs[-1])
-        for name, z in (("z_k", self.z_k), ("z_v", self.z_v)):
-            if z is not None:
-                arrs.append(_host_array(z, np.int32))
-                setattr(s, name, _address(arrs[-1]))
-        return s, arrs  # keep the arrays alive for the duration of the call
+    def _c(self, names=("s_q", "s_k", "s_v", "s_o", "clip", "z_k", "z_v")):
+        """The call's scale struct (only the named arrays that are given, the others null)
+        and those arrays by name, to be kept alive for the duration of the call."""
+        s, arrs = _Scales(), {}
+        s.per_head = bool(self.per_head)
+        for n in names:
+            x = getattr(self, n)
+            if x is not None:
+                a = arrs[n] = _host_array(x, _I32 if n in ("z_k", "z_v") else _F32)
+                setattr(s, "clip_c" if n == "clip" else n, _address(a))
+        return s, arrs
+
+    def _c_heads(self, n_q: int, n_kv: int, names):
+        """_c of the named arrays, which hold an entry per head (n_q query
+        heads, n_kv K / V heads), or one each."""
+        s, arrs = self._c(names)
+        for n, a in arrs.items():
+            want = (n_q if n in ("s_q", "s_o", "clip") else n_kv) if self.per_head else 1
+            if a.size < want:
+                raise ValueError(f"scales.{n} holds {a.size} entries; {want} are needed")
+        return s, arrs
 
 
 _lib = None
@@ -551,19 +562,6 @@ def _on(device, stream):
     return _On(device, stream)
 
 
-def _check_entries(scales: Scales, n_q: int, n_kv: int, names):
-    """The named scale arrays hold an entry per head (n_q query heads, n_kv
-    K / V heads), or one each."""
-    for name in names:
-        x = getattr(scales, name)
-        if x is None:
-            continue
-        want = (n_q if name in ("s_q", "s_o", "clip") else n_kv) if scales.per_head else 1
-        n = x.size if type(x) is np.ndarray else np.size(x)
-        if n < want:
-            raise ValueError(f"scales.{name} holds {n} entries; {want} are needed")
-
-
 def _rows(t, name: str, device, dtype) -> _Rows:
     """A [B, heads, L, d] fp16 / bf16 CUDA tensor whose channels are contiguous."""
     import torch
@@ -614,18 +612,23 @@ class RopeNorm:
     eps: float = 1e-6
     interleaved: bool = False
 
+    @staticmethod
+    def _weight(w, name: str, d: int, device) -> int:
+        import torch
+        if not isinstance(w, torch.Tensor) or w.dtype != torch.float32 or w.device != device:
+            raise TypeError(f"{name} must be a float32 tensor on {device}")
+        if w.shape != (d,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [{d}]")
+        return w.data_ptr()
+
     def _c(self, B: int, L: int, d: int, device) -> _RopeNorm:
         import torch
         c = _RopeNorm()
         c.eps, c.interleaved = self.eps, bool(self.interleaved)
-        for name in ("w_q", "w_k"):
-            w = getattr(self, name)
-            if w is not None:
-                if not isinstance(w, torch.Tensor) or w.dtype != torch.float32 or w.device != device:
-                    raise TypeError(f"{name} must be a float32 tensor on {device}")
-                if w.shape != (d,) or not w.is_contiguous():
-                    raise ValueError(f"{name} must be contiguous [{d}]")
-                setattr(c, name, w.data_ptr())
+        if self.w_q is not None:
+            c.w_q = self._weight(self.w_q, "w_q", d, device)
+        if self.w_k is not None:
+            c.w_k = self._weight(self.w_k, "w_k", d, device)
         if self.table is not None:
             t = self.table
             if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device:
@@ -732,11 +735,10 @@ def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bit
             raise ValueError("q must be [B, H, L, d] matching k")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check_entries(scales, H, Hkv, ("s_k", "s_v", "z_k", "z_v") + (("s_q",) if q is not None else ()))
     sp = _index_tensor(start, "start", (B,), dev)
     lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
     c = None if norm is None else norm._c(B, L, d, dev)
-    sc, keep = scales._c()
+    sc, keep = scales._c_heads(H, Hkv, ("s_k", "s_v", "z_k", "z_v") if q is None else ("s_k", "s_v", "z_k", "z_v", "s_q"))
     with _on(dev, stream) as st:
         if q is not None:
             if q_out is None:
@@ -777,10 +779,9 @@ def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bi
     dt = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
     if dt not in _row_types():
         raise TypeError("dtype must be float16 or bfloat16")
-    _check_entries(scales, 0, Hkv, ("s_k", "z_k") + (("s_v", "z_v") if v_cache is not None else ()))
     sp = _index_tensor(start, "start", (B,), dev)
     lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
-    sc, keep = scales._c()
+    sc, keep = scales._c_heads(0, Hkv, ("s_k", "z_k") if v_cache is None else ("s_k", "s_v", "z_k", "z_v"))
     with _on(dev, stream) as st:
         if k_out is None:
             k_out = k_cache.new_empty((B, Hkv, L, d), dtype=dt)
@@ -835,13 +836,12 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lengths, scales: Scal
     if Hkv < 1 or H % Hkv:
         raise ValueError("the query heads must be a multiple of the K / V heads")
     Lp = Lp_max if prefix_len is None else int(prefix_len)
-    _check_entries(scales, H, Hkv, ("s_q", "s_k", "s_v", "s_o", "clip", "z_k", "z_v"))
     lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
     dt = dtype or (out.dtype if out is not None else torch.int8)
     kinds = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16, torch.int8: DTYPE_INT8}
     if dt not in kinds:
         raise TypeError("dtype must be int8, float16 or bfloat16")
-    sc, keep = scales._c()
+    sc, keep = scales._c_heads(H, Hkv, ("s_q", "s_k", "s_v", "s_o", "clip", "z_k", "z_v"))
     with _on(dev, stream) as st:
         if out is None:
             out = q.new_empty((B, H, 1, d), dtype=dt)
