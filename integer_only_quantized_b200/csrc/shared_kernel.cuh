@@ -221,7 +221,9 @@ __device__ __forceinline__ int own_rows(const SharedArgs& a, int b) {
 // The blocks of `keys` own rows of every sequence and unit (K / V head, group
 // of eight query heads), in the order (b, unit, block), and a warp's
 // place among them.  Warp-collective.
-constexpr int kUnitCost = 2;  // blocks' worth of work in changing the unit, for equal shares
+// Blocks' worth of work in changing the unit, for equal shares.  LLaMA-7B heads, B64,
+// up to 777 own keys: 67.4 us a call; with 1 69.5 us.  B64 H32/8, up to 1024 own keys: 47.3 us; with 3 48.0 us.
+constexpr int kUnitCost = 2;
 struct Walk {
   int b, hk, g, blk, nb;  // sequence, K / V head, group of eight query heads; nb: blocks of the sequence
   // the share of warp `w` of `warps`: its first block (where there is one), and their number
@@ -365,8 +367,9 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int c) {
 // ---- phase A of the own rows: scores and row max of the n blocks from w ----
 // A = K: sixteen keys by 32 channels per product; B: the unit's queries.  A key
 // past the sequence's last (in a started 16-key step) gets the lowest score, whose table
-// entry is 0.  The next step's fragments are read before this one's scores
-// are stored (with two own warps per scheduler the loop is bound by latency).
+// entry is 0.  The loop is as short as it can be: with the next step's fragments read
+// ahead (more code) LLaMA-7B heads, B64, 4001 shared and up to 777 own keys took 69.5 us
+// a call instead of 67.5.
 template <int D>
 __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRing& ring, Walk w, int n) {
   constexpr int kKeys = kOwnBytes / D;
@@ -382,13 +385,7 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
 #pragma unroll 1
   for (uint32_t i = 0; i < ring.slots; ++i)
     if (left > 0) issue();
-  uint32_t k[kK][4];  // fragments of the next step
   uint32_t tile = 0;
-  bool fresh = false;  // k holds them
-  auto read = [&](int s) {
-#pragma unroll
-    for (int c = 0; c < kK; ++c) ldmatrix4(k[c], tile_at<D>(tile, 16 * s + (lane & 15), 2 * c + (lane >> 4)));
-  };
   while (n > 0) {
     Unit x;
     x.set(a, w);
@@ -407,30 +404,20 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
     const int s0 = w.blk * kSub, s1 = (w.blk + run) * kSub;
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-      if (!fresh) {
-        if ((tile = ring.wait()) == 0) return false;
-        read(0);
-        fresh = true;
-      }
+      const int in = s % kSub;
+      if (in == 0 && (tile = ring.wait()) == 0) return false;
+      uint32_t k[kK][4];
+#pragma unroll
+      for (int c = 0; c < kK; ++c) ldmatrix4(k[c], tile_at<D>(tile, 16 * in + (lane & 15), 2 * c + (lane >> 4)));
       int32_t d[2][4];  // two chains of products
 #pragma unroll
       for (int c = 0; c < 2; ++c) d[c][0] = d[c][1] = d[c][2] = d[c][3] = 0;
 #pragma unroll
       for (int c = 0; c < kK; ++c)
         mma16832(d[c & 1], k_u8, k[c][0], k[c][1], k[c][2], k[c][3], q[c][0], q[c][1]);
-      // the next fragments, before the scores are stored
-      const int in = (s + 1) % kSub;
-      if (in != 0) {
-        read(in);
-      } else {
+      if (in == kSub - 1) {
         __syncwarp();  // every lane has read the tile
         if (left > 0) issue();
-        fresh = false;
-        if (s + 1 < s1) {
-          if ((tile = ring.wait()) == 0) return false;
-          read(0);
-          fresh = true;
-        }
       }
       // d[..][0], [1]: key n8, rows 2t and 2t + 1; [2], [3]: key n8 + 8
 #pragma unroll
@@ -474,49 +461,44 @@ struct RowIndex {
 };
 
 // ---- phase B of the own rows: Z and the index bytes of the same blocks ----
-// Thread t of four takes four scores of a 16-key block; the eight lane groups
-// take the unit's rows, and with fewer than eight rows several blocks.  Two
-// batches of loads in flight.
+// Thread t of four takes four scores of a 16-key step; the eight lane groups
+// take the unit's rows, and with fewer than eight rows several steps.  The next
+// step's scores are on their way while this one's are worked on.  One step per turn of
+// the loop: with four unrolled (more loads in flight, more code to fetch)
+// LLaMA-7B heads, B64, 4001 shared and up to 777 own keys took 72.2 us a call instead of 70.3.
 template <int D>
 __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDev* hp_s, const uint32_t* lut_s, Walk w,
                                          int n) {
   constexpr int kKeys = kOwnBytes / D;
   constexpr int kSub = kKeys / 16;
-  constexpr int kBatch = 4;
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
   while (n > 0) {
     const int run = min(n, w.nb - w.blk);  // blocks of this unit
     Unit x;
     x.set(a, w);
-    const int rp = x.rows > 4 ? 8 : x.rows > 2 ? 4 : x.rows;  // lane groups per block
-    const int par = 8 / rp;                                   // blocks side by side
+    const int rp = x.rows > 4 ? 8 : x.rows > 2 ? 4 : x.rows;  // lane groups per step
+    const int par = 8 / rp;                                   // steps side by side
     const int mine = min(n8 % rp, x.rows - 1);
     const bool live = n8 % rp < x.rows;
-    const int s0 = w.blk * kSub + n8 / rp, s1 = min((w.blk + run) * kSub, (x.len + 15) / 16);  // started blocks
+    const int s1 = min((w.blk + run) * kSub, (x.len + 15) / 16);  // started steps
     const size_t row = static_cast<size_t>(x.row + mine) * a.ld_s + 4 * t;
     const int4* sp = reinterpret_cast<const int4*>(a.scores + row);
     uint32_t* ip = a.index + row / 4;
-    auto load = [&](int4 (&v)[kBatch], int s) {
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        v[k] = s + k * par < s1 ? sp[4 * (s + k * par)] : make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
-    };
-    int4 v[kBatch], nx[kBatch];
-    load(v, s0);
+    auto load = [&](int s) { return s < s1 ? sp[4 * s] : make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN); };
+    int s = w.blk * kSub + n8 / rp;
+    int4 v = load(s);
     const HeadParamsDev hp = hp_s[a.per_head ? x.head + mine : 0];
     const uint32_t* lut = lut_s + 32 * hp.lut;
     RowIndex index;
     index.set(hp, unbias(__ldcg(a.row_max + x.at + mine)));
     uint32_t z = 0;
-    for (int s = s0; s < s1; s += kBatch * par) {
-      load(nx, s + kBatch * par);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const uint32_t i0 = index(v[k].x), i1 = index(v[k].y), i2 = index(v[k].z), i3 = index(v[k].w);
-        z += (lut[i0] + lut[i1]) + (lut[i2] + lut[i3]);
-        if (live && s + k * par < s1) ip[4 * (s + k * par)] = prefill::pack4(i0, i1, i2, i3);
-        v[k] = nx[k];
-      }
+#pragma unroll 1
+    for (; s < s1; s += par) {
+      const int4 nx = load(s + par);
+      const uint32_t i0 = index(v.x), i1 = index(v.y), i2 = index(v.z), i3 = index(v.w);
+      z += (lut[i0] + lut[i1]) + (lut[i2] + lut[i3]);
+      if (live) ip[4 * s] = prefill::pack4(i0, i1, i2, i3);
+      v = nx;
     }
     __syncwarp();
     z += __shfl_xor_sync(0xffffffffu, z, 1);
@@ -545,8 +527,9 @@ __device__ __forceinline__ int own_pv_start(const SharedArgs& a, OwnRing& ring, 
 
 // ---- phase C of the own rows: P.V of the same blocks ----
 // A = V^T: sixteen channels by 32 keys per product, transposed on the way from
-// shared memory; B = P: query row n8, keys 4 t .. + 3 and 16 + 4 t .. + 3.  P of the
-// next 32 keys is made while this one's V is read.
+// shared memory; B = P: query row n8, keys 4 t .. + 3 and 16 + 4 t .. + 3, made
+// while V is read (made a step ahead, with more code: 71.2 us a call instead of 69.7
+// in the case above).
 template <int D>
 __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& ring, const HeadParamsDev* hp_s,
                                        const uint32_t* lut_s, Walk w, Walk ld, int left, int n) {
@@ -563,9 +546,8 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& 
     const int run = min(n, w.nb - w.blk);  // blocks of this unit
     n -= run;
     const int s0 = w.blk * kStep, s1 = (w.blk + run) * kStep;
-    // of the next 32 keys and the 32 after them
-    uint32_t ix0 = index_word(2 * s0), ix1 = index_word(2 * s0 + 1);
-    uint32_t iy0 = index_word(2 * s0 + 2), iy1 = index_word(2 * s0 + 3);
+    // of the next 32 keys
+    uint32_t iy0 = index_word(2 * s0), iy1 = index_word(2 * s0 + 1);
     const uint32_t R = static_cast<uint32_t>(exact_R(__ldcg(a.row_z + x.at + mine)));  // < 2^25: Z >= 2^15
     const uint32_t lut = smem_u32(lut_s) + 128 * hp_s[a.per_head ? x.head + mine : 0].lut;
     uint32_t psum = 0;
@@ -585,23 +567,24 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& 
       psum = __dp4a(p, 0x01010101u, psum);
       return p;
     };
-    uint32_t p0 = make_p(ix0), p1 = make_p(ix1), tile = 0;
+    uint32_t tile = 0;
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-      ix0 = iy0;
-      ix1 = iy1;
-      iy0 = index_word(2 * s + 4);
-      iy1 = index_word(2 * s + 5);
+      const uint32_t ix0 = iy0, ix1 = iy1;
+      iy0 = index_word(2 * s + 2);
+      iy1 = index_word(2 * s + 3);
       const int in = s % kStep;
       if (in == 0 && (tile = ring.wait()) == 0) return false;
-      uint32_t n0 = 0, n1 = 0;
+      uint32_t p0 = 0, p1 = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // half of the channels at a time
         uint32_t v[kM / 2][4];
 #pragma unroll
         for (int c = 0; c < kM / 2; ++c) ldmatrix2_trans(v[c], tile_at<D>(tile, 32 * in + lane, h * (kM / 2) + c));
-        if (h == 0) n0 = make_p(ix0);
-        else n1 = make_p(ix1);
+        if (h == 0) {
+          p0 = make_p(ix0);
+          p1 = make_p(ix1);
+        }
         if (h == 1 && in == kStep - 1) {
           __syncwarp();  // every lane has read the tile
           if (left > 0) {
@@ -613,10 +596,6 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& 
         for (int c = 0; c < kM / 2; ++c)
           mma16832_pv(o[h * (kM / 2) + c], v_u8, v[c][0], v[c][1], v[c][2], v[c][3], p0, p1);
       }
-      // P past the run belongs to no step of this unit here: not counted below
-      if (s + 1 == s1) psum -= __dp4a(n0, 0x01010101u, __dp4a(n1, 0x01010101u, 0u));
-      p0 = n0;
-      p1 = n1;
     }
     if (v_u8) {
       psum += __shfl_xor_sync(0xffffffffu, psum, 1);
