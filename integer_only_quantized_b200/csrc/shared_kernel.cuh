@@ -226,7 +226,8 @@ __device__ __forceinline__ int own_rows(const SharedArgs& a, int b) {
 constexpr int kUnitCost = 2;
 struct Walk {
   int b, hk, g, blk, nb;  // sequence, K / V head, group of eight query heads; nb: blocks of the sequence
-  // the share of warp `w` of `warps`: its first block (where there is one), and their number
+  // Goes to the start of the share of warp `w` of `warps`; its cost, 0 when there is nothing in it.
+  // A unit costs its blocks and kUnitCost; a block belongs to the share in which it starts.
   __device__ __forceinline__ int share(const SharedArgs& a, int keys, int w, int warps) {
     const int lane = threadIdx.x & 31;
     const int groups = (a.G + 7) / 8, units = a.Hkv * groups;
@@ -236,56 +237,48 @@ struct Walk {
     for (int i = lane; i < a.B; i += 32) total += cost(blocks(i));
     total = __reduce_add_sync(0xffffffffu, total) * units;
     const int each = total / warps, more = total - each * warps;
-    const int first = each * w + min(w, more);
-    int n = 0, u = 0;
+    int left = each + (w < more ? 1 : 0);
+    int p = each * w + min(w, more);  // from sequence b0 on
     b = hk = g = blk = nb = 0;
-    // the share's end, then its start: the blocks before them, and where they are
+    if (left == 0) return 0;
 #pragma unroll 1
-    for (int e = 1; e >= 0; --e) {
-      int p = e ? first + each + (w < more ? 1 : 0) : first;  // in units of cost from sequence b0 on
-      int before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      const int mine = blocks(b0 + lane);
+      int c = cost(mine);  // summed up to and with this lane's sequence
 #pragma unroll 1
-      for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int mine = blocks(b0 + lane);
-        int c = cost(mine), k = mine;  // sums up to and with this lane's sequence
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-          const int c_up = __shfl_up_sync(0xffffffffu, c, o), k_up = __shfl_up_sync(0xffffffffu, k, o);
-          if (lane >= o) {
-            c += c_up;
-            k += k_up;
-          }
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, c * units > p);
-        if (past) {
-          const int l = __ffs(past) - 1;
-          nb = __shfl_sync(0xffffffffu, mine, l);
-          b = b0 + l;
-          const int q = p - (__shfl_sync(0xffffffffu, c, l) - cost(nb)) * units;  // within sequence b
-          u = q / cost(nb);
-          blk = q - u * cost(nb);
-          if (blk >= nb) {  // between two units: the next one's first block
-            ++u;
-            blk = 0;
-          }
-          before += (__shfl_sync(0xffffffffu, k, l) - nb) * units + u * nb + blk;
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, k, 31) * units;
-        p -= __shfl_sync(0xffffffffu, c, 31) * units;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += up;
       }
-      n = e ? before : n - before;
+      const uint32_t past = __ballot_sync(0xffffffffu, c * units > p);  // p < total: some lane's in the end
+      if (past) {
+        const int l = __ffs(past) - 1;
+        nb = __shfl_sync(0xffffffffu, mine, l);
+        b = b0 + l;
+        p -= (__shfl_sync(0xffffffffu, c, l) - cost(nb)) * units;  // within sequence b
+        break;
+      }
+      p -= __shfl_sync(0xffffffffu, c, 31) * units;
     }
-    if (n == 0) return 0;
-    const bool over = u == units;  // the first block is the next sequence's
-    if (over) {
-      --u;
+    int u = p / cost(nb);
+    blk = p - u * cost(nb);
+    const bool between = blk >= nb;  // the first block is the next unit's, or the next sequence's
+    if (between) {
+      left -= cost(nb) - blk;
       blk = nb - 1;
     }
     hk = u / groups;
     g = u - hk * groups;
-    if (over) next(a, keys);
-    return n;
+    if (left <= 0) return 0;
+    if (between) next(a, keys);
+    return left;
+  }
+  // Past `run` blocks of this unit: the cost left of `left`; at the next block while there is one.
+  __device__ __forceinline__ int skip(const SharedArgs& a, int keys, int left, int run) {
+    blk += run - 1;
+    left -= blk + 1 == nb ? run + kUnitCost : run;
+    if (left > 0) next(a, keys);
+    return left;
   }
   // to the next block (there is one)
   __device__ __forceinline__ void next(const SharedArgs& a, int keys) {
@@ -364,7 +357,7 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int c) {
   return tile + r * D + 16 * (D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3)));
 }
 
-// ---- phase A of the own rows: scores and row max of the n blocks from w ----
+// ---- phase A of the own rows: scores and row max of the share of cost n from w ----
 // A = K: sixteen keys by 32 channels per product; B: the unit's queries.  A key
 // past the sequence's last (in a started 16-key step) gets the lowest score, whose table
 // entry is 0.  The loop is as short as it can be: with the next step's fragments read
@@ -377,10 +370,10 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
   constexpr int kK = D / 32;           // products per step
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
   Walk ld = w;
-  int left = n;  // blocks not yet issued
+  int left = n;  // not yet issued
   auto issue = [&]() {
     ring.issue(&a.tm_kc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk);
-    if (--left > 0) ld.next(a, kKeys);
+    left = ld.skip(a, kKeys, left, 1);
   };
 #pragma unroll 1
   for (uint32_t i = 0; i < ring.slots; ++i)
@@ -400,7 +393,6 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
     }
     int32_t m[2] = {INT_MIN, INT_MIN};
     const int run = min(n, w.nb - w.blk);  // blocks of this unit
-    n -= run;
     const int s0 = w.blk * kSub, s1 = (w.blk + run) * kSub;
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
@@ -435,10 +427,7 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
       m[1] = imax(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
     }
     if (n8 < 2 && 2 * t + n8 < x.rows) atomicMax(a.row_max + x.at + 2 * t + n8, bias(n8 ? m[1] : m[0]));
-    if (n > 0) {
-      w.blk += run - 1;
-      w.next(a, kKeys);
-    }
+    n = w.skip(a, kKeys, n, run);
   }
   return true;
 }
@@ -505,11 +494,7 @@ __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDe
     z += __shfl_xor_sync(0xffffffffu, z, 2);
     for (int o = 4 * rp; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     if (t == 0 && n8 < x.rows) atomicAdd(a.row_z + x.at + n8, static_cast<int32_t>(z));
-    n -= run;
-    if (n > 0) {
-      w.blk += run - 1;
-      w.next(a, kKeys);
-    }
+    n = w.skip(a, kKeys, n, run);
   }
 }
 
@@ -520,9 +505,9 @@ __device__ __forceinline__ int own_pv_start(const SharedArgs& a, OwnRing& ring, 
 #pragma unroll 1
   for (uint32_t i = 0; i < ring.slots && n > 0; ++i) {
     ring.issue(&a.tm_vc, ld.blk * (kOwnBytes / D), ld.b * a.Hkv + ld.hk);
-    if (--n > 0) ld.next(a, kOwnBytes / D);
+    n = ld.skip(a, kOwnBytes / D, n, 1);
   }
-  return n;  // blocks not yet issued
+  return n;  // not yet issued
 }
 
 // ---- phase C of the own rows: P.V of the same blocks ----
@@ -544,7 +529,6 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& 
     const uint32_t* ip = a.index + static_cast<size_t>(x.row + mine) * (a.ld_s / 4) + t;
     auto index_word = [&](int s) { return 16 * s < x.len ? ip[4 * s] : 0x1F1F1F1Fu; };  // of 16-key step s
     const int run = min(n, w.nb - w.blk);  // blocks of this unit
-    n -= run;
     const int s0 = w.blk * kStep, s1 = (w.blk + run) * kStep;
     // of the next 32 keys
     uint32_t iy0 = index_word(2 * s0), iy1 = index_word(2 * s0 + 1);
@@ -589,7 +573,7 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& 
           __syncwarp();  // every lane has read the tile
           if (left > 0) {
             ring.issue(&a.tm_vc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk);
-            if (--left > 0) ld.next(a, kKeys);
+            left = ld.skip(a, kKeys, left, 1);
           }
         }
 #pragma unroll
@@ -612,10 +596,7 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& 
 #pragma unroll
           for (int e = 0; e < 2; ++e) atomicAdd(dst + 16 * c + 8 * e, static_cast<float>(o[c][2 * e + r]));
       }
-    if (n > 0) {
-      w.blk += run - 1;
-      w.next(a, kKeys);
-    }
+    n = w.skip(a, kKeys, n, run);
   }
   return true;
 }
