@@ -670,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   const int RF = kBM / F;       // lanes per fold
   const uint32_t stages = args.stages;  // at least 4: the key tiles of a tile fit the ring
   const int psets = kPBufs / F; // sets of F P buffers
+  const int set_bits = F == 1 ? 2 : F == 2 ? 1 : 0;
   // this CTA's tiles
   const int t0 = static_cast<int>(static_cast<long long>(args.tiles) * blockIdx.x / gridDim.x);
   const int t1 = static_cast<int>(static_cast<long long>(args.tiles) * (blockIdx.x + 1) / gridDim.x);
@@ -955,11 +956,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
                 for (int q = 0; q < kChunk / 4; ++q) psum = __dp4a(pw[q], 0x01010101u, psum);
               }
               // The set's last P.V has read it.  With one set (F = 4) that was the
-              // other team's: this team's own P.V before it is waited for first,
-              // since a parity says nothing about a phase two ahead of the last one seen.
-              if (c == 0 && ((psets == 1 && pi >= 2 && !mbar_wait_warp(bar(kBarPEmpty), pi & 1, kRoleSoftmax)) ||
-                             !mbar_wait_warp(bar(kBarPEmpty + set), ((pi / psets) & 1) ^ 1, kRoleSoftmax)))
-                ok = false;
+              // other team's, tile pi - 1, and the P.V of even and of odd tiles complete
+              // a barrier each: a parity tells only two states apart, and at this
+              // point the P.V of tile pi - 2 may be done or not.
+              if (c == 0) {
+                const uint32_t e = psets == 1 ? (pi & 1) ^ 1 : set;
+                const uint32_t phase = psets == 1 ? ((pi + 1) >> 1) - 1 : (pi >> set_bits) - 1;  // pi = 0 .. psets - 1: none yet
+                if (!mbar_wait_warp(bar(kBarPEmpty + e), phase & 1, kRoleSoftmax)) ok = false;
+              }
               st_cols(tlane + kColP + pb * 32 + half * (kCols / 4) + c * (kChunk / 4), pw);
             });
             if (!got) ok = false;
@@ -1155,7 +1159,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
         }
       } else {
         const uint32_t idesc = idesc_i8(kBM, D, 0, v_u8 ? 0u : 1u, 1);
-        const int set_bits = F == 1 ? 2 : F == 2 ? 1 : 0;  // of the P sets
         uint32_t pc = 0, no = 0;
         // K tiles of phases A and B
         uint32_t before = 0;
@@ -1189,7 +1192,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
               taken();
             }
             if (!ok) break;
-            mma_commit(bar(kBarPEmpty + set));
+            mma_commit(bar(kBarPEmpty + (psets == 1 ? pc & 1 : set)));
             if (j == sg.n - 1) mma_commit(bar(kBarOFull));
             ++pc;
           }

@@ -384,3 +384,29 @@ def test_output_over_the_queries(ia, oracle_mod):
         q, kp, vp, kc, vc, ln = c.dev()
         ia.decode_shared(q, kp, vp, kc, vc, ln, c.scales(ia), c.clip, out=q)
         _equal(q, c.want(oracle_mod))
+
+
+@pytest.mark.parametrize("shape", [(4, 20, 37277, 229, 64), (7, 29, 15104, 60, 128), (5, 18, 12841, 300, 128),
+                                   (1, 26, 37329, 20, 64), (32, 19, 4000, 21, 64)],
+                         ids=lambda s: "B{}H{}p{}m{}d{}".format(*s))
+def test_many_tiles_of_few_queries(ia, shape):
+    """Four key tiles side by side and many tiles per CTA, over and over (the
+    softmax teams run ahead of each other in any order): the bytes of decode
+    on the joined cache."""
+    import torch
+    B, H, Lp, Lmax, d = shape
+    g = torch.Generator(device="cuda")
+    g.manual_seed(Lp)
+    mk = lambda *s: torch.randn(s, generator=g, device="cuda").mul_(28).round_().clamp_(-127, 127).to(torch.int8)
+    q, kp, vp, kc, vc = mk(B, H, 1, d), mk(H, Lp, d), mk(H, Lp, d), mk(B, H, Lmax, d), mk(B, H, Lmax, d)
+    s = 3 ** 0.5 / 28
+    sc = ia.Scales(s, s, 1 / 28, 3 / 127)
+    ln = torch.randint(0, Lmax + 1, (B,), device="cuda", dtype=torch.int32, generator=g)
+    got = [ia.decode_shared(q, kp, vp, kc, vc, ln, sc, 10.0) for _ in range(20)]
+    assert ia.device_error() == ia.OK
+    assert all(torch.equal(x, got[0]) for x in got)
+    for b in {0, B - 1}:
+        n = int(ln[b])
+        join = lambda p, c: torch.cat([p, c[b, :, :n]], 1)[None].contiguous()
+        want = ia.decode(q[b:b + 1], join(kp, kc), join(vp, vc), sc, Lp + n, 10.0)
+        assert torch.equal(got[0][b:b + 1], want)
