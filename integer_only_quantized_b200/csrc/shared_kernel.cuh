@@ -78,6 +78,7 @@ struct SharedArgs {
   int32_t key_tiles;             // 128-key tiles of the prefix
   int32_t row_tiles, seg_tiles;  // 128-row tiles of R; tiles per (head, row tile): ceil(key_tiles / F)
   int32_t tiles;                 // Hkv * row_tiles * seg_tiles
+  int32_t none;                  // 0 (see OwnRing)
   float s_o[INTATTN_MAX_HEADS];
   uint32_t lut[INTATTN_MAX_CLIPS][32];
   HeadParamsDev hp[INTATTN_MAX_HEADS];
@@ -309,16 +310,20 @@ struct Unit {
   }
 };
 
-// A warp's private ring of blocks for the own rows' tiles.
+// A warp's private ring of blocks for the own rows' tiles.  The warp that reads a
+// block also starts the copy that replaces it, and nothing but a dependency orders a
+// copy behind reads that are still on their way to registers (the two take
+// different paths; with other warps keeping shared memory busy a copy did overtake them).  So
+// `issue` takes a value made of what was read: `read` & args.none, which is 0 when it arrives.
 struct OwnRing {
   uint32_t base, bar;    // shared addresses: slot i at base + kOwnBytes i, barrier i at bar + 8 i
   uint32_t slots;
   uint32_t issued, used; // tiles, both counted over the slots as 2 slots states
   __device__ __forceinline__ uint32_t step(uint32_t n) const { return n + 1 == 2 * slots ? 0u : n + 1; }
   __device__ __forceinline__ uint32_t slot(uint32_t n) const { return n < slots ? n : n - slots; }
-  __device__ __forceinline__ void issue(const CUtensorMap* tm, int y, int z) {
+  __device__ __forceinline__ void issue(const CUtensorMap* tm, int y, int z, uint32_t zero) {
     const uint32_t i = slot(issued);
-    tma_load_3d_elect(base + kOwnBytes * i, tm, bar + 8 * i, kOwnBytes, 0, y, z);
+    tma_load_3d_elect(base + kOwnBytes * i + zero, tm, bar + 8 * i + zero, kOwnBytes, 0, y, z);
     issued = step(issued);
   }
   // the oldest tile not yet used (its address), or 0 when the wait ran out
@@ -371,13 +376,13 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
   const int lane = threadIdx.x & 31, n8 = lane >> 2, t = lane & 3;
   Walk ld = w;
   int left = n;  // not yet issued
-  auto issue = [&]() {
-    ring.issue(&a.tm_kc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk);
+  auto issue = [&](uint32_t read) {
+    ring.issue(&a.tm_kc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk, read & a.none);
     left = ld.skip(a, kKeys, left, 1);
   };
 #pragma unroll 1
   for (uint32_t i = 0; i < ring.slots; ++i)
-    if (left > 0) issue();
+    if (left > 0) issue(0u);
   uint32_t tile = 0;
   while (n > 0) {
     Unit x;
@@ -407,9 +412,11 @@ __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRi
 #pragma unroll
       for (int c = 0; c < kK; ++c)
         mma16832(d[c & 1], k_u8, k[c][0], k[c][1], k[c][2], k[c][3], q[c][0], q[c][1]);
-      if (in == kSub - 1) {
-        __syncwarp();  // every lane has read the tile
-        if (left > 0) issue();
+      if (in == kSub - 1 && left > 0) {
+        uint32_t read = 0;
+#pragma unroll
+        for (int c = 0; c < kK; ++c) read |= k[c][0] | k[c][1] | k[c][2] | k[c][3];
+        issue(read);
       }
       // d[..][0], [1]: key n8, rows 2t and 2t + 1; [2], [3]: key n8 + 8
 #pragma unroll
@@ -504,7 +511,7 @@ template <int D>
 __device__ __forceinline__ int own_pv_start(const SharedArgs& a, OwnRing& ring, Walk& ld, int n) {
 #pragma unroll 1
   for (uint32_t i = 0; i < ring.slots && n > 0; ++i) {
-    ring.issue(&a.tm_vc, ld.blk * (kOwnBytes / D), ld.b * a.Hkv + ld.hk);
+    ring.issue(&a.tm_vc, ld.blk * (kOwnBytes / D), ld.b * a.Hkv + ld.hk, 0u);
     n = ld.skip(a, kOwnBytes / D, n, 1);
   }
   return n;  // not yet issued
@@ -559,7 +566,7 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& 
       iy1 = index_word(2 * s + 3);
       const int in = s % kStep;
       if (in == 0 && (tile = ring.wait()) == 0) return false;
-      uint32_t p0 = 0, p1 = 0;
+      uint32_t p0 = 0, p1 = 0, read = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // half of the channels at a time
         uint32_t v[kM / 2][4];
@@ -569,16 +576,15 @@ __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& 
           p0 = make_p(ix0);
           p1 = make_p(ix1);
         }
-        if (h == 1 && in == kStep - 1) {
-          __syncwarp();  // every lane has read the tile
-          if (left > 0) {
-            ring.issue(&a.tm_vc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk);
-            left = ld.skip(a, kKeys, left, 1);
-          }
-        }
 #pragma unroll
-        for (int c = 0; c < kM / 2; ++c)
+        for (int c = 0; c < kM / 2; ++c) {
           mma16832_pv(o[h * (kM / 2) + c], v_u8, v[c][0], v[c][1], v[c][2], v[c][3], p0, p1);
+          read |= v[c][0] | v[c][1] | v[c][2] | v[c][3];
+        }
+      }
+      if (in == kStep - 1 && left > 0) {
+        ring.issue(&a.tm_vc, ld.blk * kKeys, ld.b * a.Hkv + ld.hk, read & a.none);
+        left = ld.skip(a, kKeys, left, 1);
       }
     }
     if (v_u8) {

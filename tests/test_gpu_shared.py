@@ -410,3 +410,28 @@ def test_many_tiles_of_few_queries(ia, shape):
         join = lambda p, c: torch.cat([p, c[b, :, :n]], 1)[None].contiguous()
         want = ia.decode(q[b:b + 1], join(kp, kc), join(vp, vc), sc, Lp + n, 10.0)
         assert torch.equal(got[0][b:b + 1], want)
+
+
+@pytest.mark.parametrize("shape", [(45, 18, 95, 555, 64), (64, 32, 200, 777, 128), (60, 8, 1500, 1000, 64)],
+                         ids=lambda s: "B{}H{}p{}m{}d{}".format(*s))
+def test_own_blocks_are_not_replaced_while_read(ia, shape):
+    """Own rows streaming beside a busy prefix, over and over: always the
+    bytes of the first call, and of decode on the joined cache."""
+    import torch
+    B, H, Lp, Lmax, d = shape
+    g = torch.Generator(device="cuda")
+    g.manual_seed(Lmax)
+    mk = lambda *s: torch.randn(s, generator=g, device="cuda").mul_(28).round_().clamp_(-127, 127).to(torch.int8)
+    q, kp, vp, kc, vc = mk(B, H, 1, d), mk(H, Lp, d), mk(H, Lp, d), mk(B, H, Lmax, d), mk(B, H, Lmax, d)
+    s = 3 ** 0.5 / 28
+    sc = ia.Scales(s, s, 1 / 28, 3 / 127)
+    ln = torch.randint(0, Lmax + 1, (B,), device="cuda", dtype=torch.int32, generator=g)
+    first = ia.decode_shared(q, kp, vp, kc, vc, ln, sc, 10.0)
+    for _ in range(200):
+        assert torch.equal(ia.decode_shared(q, kp, vp, kc, vc, ln, sc, 10.0), first)
+    assert ia.device_error() == ia.OK
+    for b in range(0, B, 13):
+        n = int(ln[b])
+        join = lambda p, c: torch.cat([p, c[b, :, :n]], 1)[None].contiguous()
+        want = ia.decode(q[b:b + 1], join(kp, kc), join(vp, vc), sc, Lp + n, 10.0)
+        assert torch.equal(first[b:b + 1], want)
