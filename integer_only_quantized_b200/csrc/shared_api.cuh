@@ -165,7 +165,9 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int sms = 0;
   if (sm_count(&sms) != INTATTN_OK) return INTATTN_ERR_CUDA;
-  // few queries fold F key tiles into a tile, as long as every SM still gets one
+  // Few queries fold F key tiles into a tile, as long as every SM still gets
+  // one: B9 H32/8 d128 over 50000 shared keys 54 us a call, without folding 65 us;
+  // B4 H12 d64 over 500 (too few tiles) 17.8 us, folded all the same 18.4 us.
   a.fold = 1;
   for (int f = 2; f <= 4; f *= 2)
     if (a.R <= intattn::shared::kBM / f && static_cast<long long>(Hkv) * ((a.key_tiles + f - 1) / f) >= sms) a.fold = f;
@@ -182,7 +184,8 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
     return INTATTN_ERR_CUDA;
   // The K / V ring and the own warps' rings share their memory (kRingBytes):
   // one block per own warp instead of two where the prefix is the longer stream
-  // (B9 H32/8 over 50000 shared and up to 333 own keys: @@ us against @@).
+  // (B9 H32/8 over 50000 shared and up to 333 own keys: 53.9 us against 54.7 with
+  // two; one everywhere: B64 H32, 4001 shared and up to 777 own keys 90 us against 73).
   const long long own_keys = static_cast<long long>(B) * Hkv * Lmax, prefix_keys = static_cast<long long>(Hkv) * Lp;
   a.own_slots = Lmax == 0 ? 0 : 2 * own_keys <= prefix_keys ? 1 : 2;
   a.stages = (intattn::shared::kRingBytes - a.own_slots * intattn::shared::kOwnWarps * intattn::shared::kOwnBytes) /

@@ -41,6 +41,19 @@
 // the 16 side and the grouped heads on the 8 side.  Scores
 // (4 bytes per key and head), and from phase B on their table indices (one
 // byte), wait in the workspace; a warp reads back what it wrote itself.
+//
+// Measured, per call in a CUDA graph (zero kernel and this one; own lengths
+// uniform up to the number given), beside the time of a copy of the bytes:
+//   B4 H12/12 d64, 500 shared, 64 own            17.8 us   (launches and three
+//                                                phases of one tile each)
+//   B64 H32/8 d128, 8192 shared, 1024 own        49 us     12.9 us
+//   B64 H32/32 d128 u8, 4001 shared, 777 own     68 us     36.3 us (3.5 TB/s)
+//   B9 H32/8 d128, 50000 shared, 333 own         54 us     16.1 us
+// Bound: the three dependent phases (scores of the prefix are made three
+// times), in each the latency of the softmax warps' loops and of fetching them: the issue
+// slots are a third used, the tensor pipe 9 to 20 %, DRAM 20 to 43 %.  Every
+// change that made a loop's code smaller made it faster, and unrolling,
+// reading ahead and prefetching V into L2 during phase B made it slower.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -1103,7 +1116,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     // other's slots.  What lies between two tiles' products is the latency of a few
     // dependent instructions, in which the tensor pipe stands still: so one
     // thread runs the whole loop, and waits for a K or V tile only before its
-    // own products, while those of the one before it run.
+    // own products, while those of the one before it run (warp-wide loops: B9
+    // L50000 54.7 us a call instead of 53.8).  Two issuers instead of one took B64 L8192 from
+    // 52 to 50.6 us and left the other cases where they were.
     if (elect_one()) {
       const bool pv = warp == kPvWarp;
       const uint64_t kv_desc0 = smem_desc(sKV, 16, C::kSBO, C::kSwizzle);
