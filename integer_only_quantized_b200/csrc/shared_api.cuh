@@ -193,6 +193,11 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   // as many CTAs as there are prefix tiles or 128-key pieces of own rows
   const long long own = static_cast<long long>(B) * Hkv * ((Lmax + 127) / 128);
   const int grid = static_cast<int>(std::min<long long>(sms, std::max<long long>(std::max(tiles, own), 1)));
+  // A CTA whose tiles belong to two heads pays for the second segment (tables, O read out
+  // twice): four tiles' worth.  B64 H32/8 over 8192 + 1024 keys 44.9 us a call instead
+  // of 47.9, B9 L50000 50.3 instead of 54.6.  Not where a CTA has one tile at
+  // most: B4 H12 L500 17.2 us, with it 19.0 (two tiles here, none there).
+  a.seg_cost = tiles > grid ? 4 : 0;
   if (a.k_u8 || a.v_u8) return d == 64 ? shared_launch<64, true>(a, grid, L, st) : shared_launch<128, true>(a, grid, L, st);
   return d == 64 ? shared_launch<64, false>(a, grid, L, st) : shared_launch<128, false>(a, grid, L, st);
 }

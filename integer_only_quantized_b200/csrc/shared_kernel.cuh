@@ -91,6 +91,7 @@ struct SharedArgs {
   int32_t key_tiles;             // 128-key tiles of the prefix
   int32_t row_tiles, seg_tiles;  // 128-row tiles of R; tiles per (head, row tile): ceil(key_tiles / F)
   int32_t tiles;                 // Hkv * row_tiles * seg_tiles
+  int32_t seg_cost;              // of a segment, in tiles, for equal shares (see first_tile)
   int32_t none;                  // 0 (see OwnRing)
   float s_o[INTATTN_MAX_HEADS];
   uint32_t lut[INTATTN_MAX_CLIPS][32];
@@ -187,6 +188,15 @@ __device__ __forceinline__ Segment segment_at(const SharedArgs& a, int t, int t1
   s.hk = u / a.row_tiles;
   s.rt = u - s.hk * a.row_tiles;
   return s;
+}
+// Where CTA i's tiles start: equal shares of a cost that counts seg_cost tiles
+// more for each (head, row tile).
+__device__ __forceinline__ int first_tile(const SharedArgs& a, uint32_t i) {
+  if (a.tiles == 0) return 0;
+  const long long each = a.seg_tiles + a.seg_cost;
+  const long long p = static_cast<long long>(a.Hkv) * a.row_tiles * each * i / gridDim.x;
+  const int u = static_cast<int>(p / each);
+  return u * a.seg_tiles + min(static_cast<int>(p - u * each), a.seg_tiles);
 }
 // key tiles of tile j of a segment's (head, row tile)
 __device__ __forceinline__ int folds_at(const SharedArgs& a, int j) { return min(a.fold, a.key_tiles - j * a.fold); }
@@ -691,8 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
   const int psets = kPBufs / F; // sets of F P buffers
   const int set_bits = F == 1 ? 2 : F == 2 ? 1 : 0;
   // this CTA's tiles
-  const int t0 = static_cast<int>(static_cast<long long>(args.tiles) * blockIdx.x / gridDim.x);
-  const int t1 = static_cast<int>(static_cast<long long>(args.tiles) * (blockIdx.x + 1) / gridDim.x);
+  const int t0 = first_tile(args, blockIdx.x), t1 = first_tile(args, blockIdx.x + 1);
 
   // The queries of at most two segments stay in the two Q buffers through all
   // phases, loaded by the softmax warps; of more, one warp loads them again in every phase.

@@ -29,7 +29,14 @@ class Cta:
         own_slots = 0 if Lmax == 0 else 1 if 2 * B * Hkv * Lmax <= Hkv * Lp else 2
         self.stages = (144 * 1024 - own_slots * 8 * 4096) // (128 * D)
         self.psets = 4 // self.F
-        t0, t1 = tiles * cta // grid, tiles * (cta + 1) // grid
+        each = self.seg_tiles + (4 if tiles > grid else 0)
+
+        def first(i):
+            p = Hkv * row_tiles * each * i // grid
+            return p // each * self.seg_tiles + min(p % each, self.seg_tiles)
+
+        assert first(0) == 0 and first(grid) == tiles
+        t0, t1 = first(cta), first(cta + 1)
         self.q_stays = t0 < t1 and (t1 - 1) // self.seg_tiles - t0 // self.seg_tiles < 2
         self.segs = []
         while t0 < t1:
