@@ -198,6 +198,10 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   // of 47.9, B9 L50000 50.3 instead of 54.6.  Not where a CTA has one tile at
   // most: B4 H12 L500 17.2 us, with it 19.0 (two tiles here, none there).
   a.seg_cost = tiles > grid ? 4 : 0;
+  const long long cost = static_cast<long long>(Hkv) * a.row_tiles * (a.seg_tiles + a.seg_cost);
+  if (cost > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;
+  a.cta_cost = static_cast<int32_t>(cost / grid);
+  a.cta_more = static_cast<int32_t>(cost % grid);
   if (a.k_u8 || a.v_u8) return d == 64 ? shared_launch<64, true>(a, grid, L, st) : shared_launch<128, true>(a, grid, L, st);
   return d == 64 ? shared_launch<64, false>(a, grid, L, st) : shared_launch<128, false>(a, grid, L, st);
 }

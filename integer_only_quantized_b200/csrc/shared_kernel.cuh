@@ -92,6 +92,7 @@ struct SharedArgs {
   int32_t row_tiles, seg_tiles;  // 128-row tiles of R; tiles per (head, row tile): ceil(key_tiles / F)
   int32_t tiles;                 // Hkv * row_tiles * seg_tiles
   int32_t seg_cost;              // of a segment, in tiles, for equal shares (see first_tile)
+  int32_t cta_cost, cta_more;    // a CTA's share of the cost, and one more for the first cta_more
   int32_t none;                  // 0 (see OwnRing)
   float s_o[INTATTN_MAX_HEADS];
   uint32_t lut[INTATTN_MAX_CLIPS][32];
@@ -191,12 +192,12 @@ __device__ __forceinline__ Segment segment_at(const SharedArgs& a, int t, int t1
 }
 // Where CTA i's tiles start: equal shares of a cost that counts seg_cost tiles
 // more for each (head, row tile).
-__device__ __forceinline__ int first_tile(const SharedArgs& a, uint32_t i) {
+__device__ __forceinline__ int first_tile(const SharedArgs& a, int i) {
   if (a.tiles == 0) return 0;
-  const long long each = a.seg_tiles + a.seg_cost;
-  const long long p = static_cast<long long>(a.Hkv) * a.row_tiles * each * i / gridDim.x;
-  const int u = static_cast<int>(p / each);
-  return u * a.seg_tiles + min(static_cast<int>(p - u * each), a.seg_tiles);
+  const int each = a.seg_tiles + a.seg_cost;
+  const int p = a.cta_cost * i + min(i, a.cta_more);
+  const int u = p / each;
+  return u * a.seg_tiles + min(p - u * each, a.seg_tiles);
 }
 // key tiles of tile j of a segment's (head, row tile)
 __device__ __forceinline__ int folds_at(const SharedArgs& a, int j) { return min(a.fold, a.key_tiles - j * a.fold); }

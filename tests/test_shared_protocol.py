@@ -32,7 +32,8 @@ class Cta:
         each = self.seg_tiles + (4 if tiles > grid else 0)
 
         def first(i):
-            p = Hkv * row_tiles * each * i // grid
+            share, more = divmod(Hkv * row_tiles * each, grid)
+            p = share * i + min(i, more)
             return p // each * self.seg_tiles + min(p % each, self.seg_tiles)
 
         assert first(0) == 0 and first(grid) == tiles
