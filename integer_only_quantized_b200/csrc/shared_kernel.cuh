@@ -44,14 +44,14 @@
 //
 // Measured, per call in a CUDA graph (zero kernel and this one; own lengths
 // uniform up to the number given), beside the time of a copy of the bytes:
-//   B4 H12/12 d64, 500 shared, 64 own            17.8 us   (launches and three
+//   B4 H12/12 d64, 500 shared, 64 own            17.7 us   (launches and three
 //                                                phases of one tile each)
-//   B64 H32/8 d128, 8192 shared, 1024 own        49 us     12.9 us
+//   B64 H32/8 d128, 8192 shared, 1024 own        45 us     12.9 us
 //   B64 H32/32 d128 u8, 4001 shared, 777 own     68 us     36.3 us (3.5 TB/s)
-//   B9 H32/8 d128, 50000 shared, 333 own         54 us     16.1 us
+//   B9 H32/8 d128, 50000 shared, 333 own         50 us     16.1 us
 // Bound: the three dependent phases (scores of the prefix are made three
 // times), in each the latency of the softmax warps' loops and of fetching them: the issue
-// slots are a third used, the tensor pipe 9 to 20 %, DRAM 20 to 43 %.  Every
+// slots are a third used, the tensor pipe 9 to 21 %, DRAM 21 to 42 %.  Every
 // change that made a loop's code smaller made it faster, and unrolling,
 // reading ahead and prefetching V into L2 during phase B made it slower.
 #pragma once
