@@ -166,8 +166,8 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   int sms = 0;
   if (sm_count(&sms) != INTATTN_OK) return INTATTN_ERR_CUDA;
   // Few queries fold F key tiles into a tile, as long as every SM still gets
-  // one: B9 H32/8 d128 over 50000 shared keys 54 us a call, without folding 65 us;
-  // B4 H12 d64 over 500 (too few tiles) 17.8 us, folded all the same 18.4 us.
+  // one: B9 H32/8 d128 over 50000 shared keys 51 us a call, without folding 63 us;
+  // B4 H12 d64 over 500 (too few tiles) 17.2 us, folded all the same 17.5 us.
   a.fold = 1;
   for (int f = 2; f <= 4; f *= 2)
     if (a.R <= intattn::shared::kBM / f && static_cast<long long>(Hkv) * ((a.key_tiles + f - 1) / f) >= sms) a.fold = f;
@@ -184,8 +184,8 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
     return INTATTN_ERR_CUDA;
   // The K / V ring and the own warps' rings share their memory (kRingBytes):
   // one block per own warp instead of two where the prefix is the longer stream
-  // (B9 H32/8 over 50000 shared and up to 333 own keys: 53.9 us against 54.7 with
-  // two; one everywhere: B64 H32, 4001 shared and up to 777 own keys 90 us against 73).
+  // (B9 H32/8 over 50000 shared and up to 333 own keys: 51.0 us against 52.5 with
+  // two; one everywhere: B64 H32, 4001 shared and up to 777 own keys 82 us against 67.5).
   const long long own_keys = static_cast<long long>(B) * Hkv * Lmax, prefix_keys = static_cast<long long>(Hkv) * Lp;
   a.own_slots = Lmax == 0 ? 0 : 2 * own_keys <= prefix_keys ? 1 : 2;
   a.stages = (intattn::shared::kRingBytes - a.own_slots * intattn::shared::kOwnWarps * intattn::shared::kOwnBytes) /
@@ -194,9 +194,9 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   const long long own = static_cast<long long>(B) * Hkv * ((Lmax + 127) / 128);
   const int grid = static_cast<int>(std::min<long long>(sms, std::max<long long>(std::max(tiles, own), 1)));
   // A CTA whose tiles belong to two heads pays for the second segment (tables, O read out
-  // twice): four tiles' worth.  B64 H32/8 over 8192 + 1024 keys 44.9 us a call instead
-  // of 47.9, B9 L50000 50.3 instead of 54.6.  Not where a CTA has one tile at
-  // most: B4 H12 L500 17.2 us, with it 19.0 (two tiles here, none there).
+  // twice): four tiles' worth.  B64 H32/8 over 8192 + 1024 keys 44.4 us a call instead
+  // of 47.5, B9 L50000 51.0 instead of 53.9.  Not where a CTA has one tile at
+  // most: B4 H12 L500 17.2 us, with it 18.9 (two tiles here, none there).
   a.seg_cost = tiles > grid ? 4 : 0;
   const long long cost = static_cast<long long>(Hkv) * a.row_tiles * (a.seg_tiles + a.seg_cost);
   if (cost > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;

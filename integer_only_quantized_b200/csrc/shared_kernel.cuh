@@ -247,7 +247,8 @@ __device__ __forceinline__ int own_rows(const SharedArgs& a, int b) {
 // of eight query heads), in the order (b, unit, block), and a warp's
 // place among them.  Warp-collective.
 // Blocks' worth of work in changing the unit, for equal shares.  LLaMA-7B heads, B64,
-// up to 777 own keys: 67.4 us a call; with 1 69.5 us.  B64 H32/8, up to 1024 own keys: 47.3 us; with 3 48.0 us.
+// up to 777 own keys: 67.4 us a call; with 1 70.0 us.  B64 H32/8, up to 1024 own
+// keys: 44.5 us; with 3 44.9 us.
 constexpr int kUnitCost = 2;
 struct Walk {
   int b, hk, g, blk, nb;  // sequence, K / V head, group of eight query heads; nb: blocks of the sequence
