@@ -212,6 +212,14 @@ int intattn_decode_int4(const int8_t *q, const uint8_t *k_cache, const uint8_t *
  * type of intattn_decode_shared only). */
 enum { INTATTN_DTYPE_FP16 = 0, INTATTN_DTYPE_BF16 = 1, INTATTN_DTYPE_INT8 = 2 };
 
+/* Added to the dtype of intattn_qk_norm_rope, intattn_cache_write and
+ * intattn_cache_read and to the out_dtype of intattn_decode_shared: output
+ * rows that the call leaves out (padding, positions, cache rows and lengths
+ * out of range) become 0 instead of staying as they were.  For outputs in
+ * fresh memory, whose bytes a later call (a row max, say) would read.  Cache rows are left alone
+ * either way. */
+enum { INTATTN_ZERO_LEFT_OUT = 0x100 };
+
 /* Quantisation prologue (the step upstream of the integer pipeline: the
  * forum page "IntAttention：面向边缘设备的纯整数注意力推理加速方案", section
  * 动态量化策略, sets each layer's or head's range from the live activations).

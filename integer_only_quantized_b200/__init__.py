@@ -33,6 +33,7 @@ EXPORTED = ("intattn_derive_params", "intattn_forward", "intattn_forward_variant
             "intattn_gelu_derive_params", "intattn_gelu", "intattn_selftest_timeout", "intattn_device_error",
             "intattn_strerror")
 DTYPE_FP16, DTYPE_BF16, DTYPE_INT8 = 0, 1, 2
+ZERO_LEFT_OUT = 0x100
 VARIANT_AUTO, VARIANT_THREE_PASS, VARIANT_SHORT_ROWS = 0, 1, 2
 SHORT_ROWS_MAX_KEYS = 256
 
@@ -653,11 +654,12 @@ def rope_table(n_positions: int, rot: int, base: float = 10000.0, device="cuda")
     return torch.stack([a.cos(), a.sin()], dim=-1).float().contiguous()
 
 
-def _rows_out(t, name: str, like):
-    """An output of the shape and type of `like` (None: a new one) and its _Rows."""
+def _rows_out(t, name: str, like, zeroed=False):
+    """An output of the shape and type of `like` (None: a new one, cleared
+    where `zeroed`) and its _Rows."""
     if t is None:
         B, h, L, d = like.shape
-        t = like.new_empty((B, h, L, d))
+        t = (like.new_zeros if zeroed else like.new_empty)((B, h, L, d))
         return t, _Rows(t.data_ptr(), h * L * d, L * d, d)
     r = _rows(t, name, like.device, like.dtype)
     if t.shape != like.shape:
@@ -668,7 +670,9 @@ def _rows_out(t, name: str, like):
 def qk_norm_rope(q, k, norm: RopeNorm, q_out=None, k_out=None, stream=None):
     """(q_out, k_out): norm and position rotation of fp16 / bf16 q [B, H, L, d]
     and k [B, Hkv, L, d] (strided views with contiguous channels; k None:
-    queries only) in one pass.  In place: q_out=q, k_out=k."""
+    queries only) in one pass.  In place: q_out=q, k_out=k.  Rows whose
+    position is negative (padding) or past the table are left as they were in outputs that are
+    passed, and are 0 in those that are not."""
     import torch
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise TypeError("q must be a CUDA tensor [B, H, L, d]")
@@ -685,11 +689,16 @@ def qk_norm_rope(q, k, norm: RopeNorm, q_out=None, k_out=None, stream=None):
     elif k_out is not None:
         raise ValueError("k_out without k")
     c = norm._c(B, L, d, dev)
+    kind = _row_types()[dt]
+    # rows can be left out: by the kernel where both outputs are new, else in advance
+    ragged, mixed = norm.table is not None, k is not None and (q_out is None) != (k_out is None)
+    if ragged and q_out is None and not mixed:
+        kind |= ZERO_LEFT_OUT
     with _on(dev, stream) as st:
-        q_out, qor = _rows_out(q_out, "q_out", q)
+        q_out, qor = _rows_out(q_out, "q_out", q, ragged and mixed)
         if k is not None:
-            k_out, kor = _rows_out(k_out, "k_out", k)
-        _check(lib().intattn_qk_norm_rope(qr, kr, c, _row_types()[dt], B, H, Hkv, L, d, qor, kor, st), "intattn_qk_norm_rope")
+            k_out, kor = _rows_out(k_out, "k_out", k, ragged and mixed)
+        _check(lib().intattn_qk_norm_rope(qr, kr, c, kind, B, H, Hkv, L, d, qor, kor, st), "intattn_qk_norm_rope")
     return q_out, k_out
 
 
@@ -709,7 +718,8 @@ def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bit
     caches' fixed scales into cache rows start[b] + t, t < lengths[b] (int32
     CUDA [B]; None: L).  k_cache, v_cache: [B, Hkv, Lmax, d] int8 (uint8 with
     zero-points), or, bits = 4, uint8 [B, Hkv, Lmax, d/2].  q [B, H, L, d]:
-    also the step's queries, with scales.s_q, into int8 q_out (returned).
+    also the step's queries, with scales.s_q, into int8 q_out (returned; new
+    where none is passed, with 0 in the rows that are not written).
     norm: norm and rotation of q and k first, in the same pass."""
     import torch
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -739,6 +749,7 @@ def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bit
     lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
     c = None if norm is None else norm._c(B, L, d, dev)
     sc, keep = scales._c_heads(H, Hkv, ("s_k", "s_v", "z_k", "z_v") if q is None else ("s_k", "s_v", "z_k", "z_v", "s_q"))
+    kind = _row_types()[dt] | (ZERO_LEFT_OUT if q is not None and q_out is None else 0)
     with _on(dev, stream) as st:
         if q is not None:
             if q_out is None:
@@ -746,7 +757,7 @@ def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bit
             _check_tensor(q_out, "q_out")
             if q_out.shape != q.shape or q_out.device != dev:
                 raise ValueError("q_out must match q")
-        rc = lib().intattn_cache_write(kr, vr, qr, _row_types()[dt], sc, int(bits), c,
+        rc = lib().intattn_cache_write(kr, vr, qr, kind, sc, int(bits), c,
                                        B, H, Hkv, L, Lmax, d, sp, lp, k_cache.data_ptr(), v_cache.data_ptr(),
                                        None if q is None else q_out.data_ptr(), st)
     del keep
@@ -758,7 +769,8 @@ def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bi
                v_out=None, stream=None):
     """(k_out, v_out): the values of cache rows start[b] + t, t < lengths[b]
     (None: L), as fp16 / bf16 [B, Hkv, L, d] (dtype; default bf16).  Rows past
-    lengths[b] are left as they were.  v_cache None: K only."""
+    lengths[b], and those of cache rows that do not exist, are left as they were in outputs that are
+    passed, and are 0 in those that are not.  v_cache None: K only."""
     import torch
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or not k_cache.is_cuda:
         raise TypeError("k_cache must be a CUDA tensor [B, Hkv, Lmax, d]")
@@ -782,11 +794,18 @@ def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bi
     sp = _index_tensor(start, "start", (B,), dev)
     lp = None if lengths is None else _index_tensor(lengths, "lengths", (B,), dev)
     sc, keep = scales._c_heads(0, Hkv, ("s_k", "z_k") if v_cache is None else ("s_k", "s_v", "z_k", "z_v"))
+    kind = _row_types()[dt]
+    # rows left out become 0 in new outputs: by the kernel where all are new, else in advance
+    new = k_cache.new_empty
+    if v_cache is not None and (k_out is None) != (v_out is None):
+        new = k_cache.new_zeros
+    elif k_out is None:
+        kind |= ZERO_LEFT_OUT
     with _on(dev, stream) as st:
         if k_out is None:
-            k_out = k_cache.new_empty((B, Hkv, L, d), dtype=dt)
+            k_out = new((B, Hkv, L, d), dtype=dt)
         if v_out is None and v_cache is not None:
-            v_out = k_cache.new_empty((B, Hkv, L, d), dtype=dt)
+            v_out = new((B, Hkv, L, d), dtype=dt)
         for t, n in ((k_out, "k_out"), (v_out, "v_out")):
             if t is None:
                 continue
@@ -795,7 +814,7 @@ def cache_read(k_cache, v_cache, scales: Scales, start, L: int, lengths=None, bi
             if t.shape != (B, Hkv, L, d) or not t.is_contiguous():
                 raise ValueError(f"{n} must be contiguous {[B, Hkv, L, d]}")
         rc = lib().intattn_cache_read(k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), sc, int(bits),
-                                      B, Hkv, L, Lmax, d, sp, lp, _row_types()[dt],
+                                      B, Hkv, L, Lmax, d, sp, lp, kind,
                                       k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), st)
     del keep
     _check(rc, "intattn_cache_read")
@@ -813,7 +832,8 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lengths, scales: Scal
     then the first lengths[b] rows (int32 CUDA [B]; None: all) of k_cache,
     v_cache [B, Hkv, Lmax, d].  H a multiple of Hkv; scales.s_q, s_o, clip: H
     entries per head, s_k, s_v, z_k, z_v: Hkv.  dtype: torch.int8 (default),
-    the codes; float16 / bfloat16, the values they stand for."""
+    the codes; float16 / bfloat16, the values they stand for.  A length out of
+    range leaves its sequence as it was in an `out` that is passed, and 0 in one that is not."""
     import torch
     _check_tensor(q, "q")
     dev = q.device
@@ -842,6 +862,7 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lengths, scales: Scal
     if dt not in kinds:
         raise TypeError("dtype must be int8, float16 or bfloat16")
     sc, keep = scales._c_heads(H, Hkv, ("s_q", "s_k", "s_v", "s_o", "clip", "z_k", "z_v"))
+    kind = kinds[dt] | (ZERO_LEFT_OUT if out is None else 0)
     with _on(dev, stream) as st:
         if out is None:
             out = q.new_empty((B, H, 1, d), dtype=dt)
@@ -855,7 +876,7 @@ def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, lengths, scales: Scal
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         rc = lib().intattn_decode_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), Lp, Lp_max,
                                          k_cache.data_ptr(), v_cache.data_ptr(), lp, sc, B, H, Hkv, Lmax, d,
-                                         float(clip_c), kinds[dt], out.data_ptr(), workspace.data_ptr(),
+                                         float(clip_c), kind, out.data_ptr(), workspace.data_ptr(),
                                          workspace.numel() * workspace.element_size(), st)
     del keep
     _check(rc, "intattn_decode_shared")

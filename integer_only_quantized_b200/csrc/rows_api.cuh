@@ -9,6 +9,14 @@ using intattn::RowArgs;
 using intattn::RowCodeArgs;
 using intattn::RowTensor;
 
+// The element type of a call's floating tensors; whether rows left out become 0.
+bool row_dtype(int dtype, int32_t* bf16, int32_t* zero) {
+  *zero = dtype >= 0 && (dtype & INTATTN_ZERO_LEFT_OUT) ? 1 : 0;
+  if (*zero) dtype &= ~INTATTN_ZERO_LEFT_OUT;
+  *bf16 = dtype == INTATTN_DTYPE_BF16 ? 1 : 0;
+  return dtype == INTATTN_DTYPE_FP16 || dtype == INTATTN_DTYPE_BF16;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A strided [B, heads, L, d] tensor of 16-bit elements whose rows start on
@@ -107,7 +115,8 @@ int intattn_qk_norm_rope(const intattn_rows_t* q, const intattn_rows_t* k, const
       (k != nullptr) != (k_out != nullptr))
     return INTATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return INTATTN_ERR_UNSUPPORTED;
-  if (dtype != INTATTN_DTYPE_FP16 && dtype != INTATTN_DTYPE_BF16) return INTATTN_ERR_UNSUPPORTED;
+  int32_t bf16, zero;
+  if (!row_dtype(dtype, &bf16, &zero)) return INTATTN_ERR_UNSUPPORTED;
   if (H > 65535 || Hkv > 65535) return INTATTN_ERR_UNSUPPORTED;
   RowArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -130,7 +139,8 @@ int intattn_qk_norm_rope(const intattn_rows_t* q, const intattn_rows_t* k, const
   }
   a.B = B;
   a.L = L;
-  a.bf16 = dtype == INTATTN_DTYPE_BF16 ? 1 : 0;
+  a.bf16 = bf16;
+  a.zero_left_out = zero;
   return rows_launch<false>(a, d, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -141,7 +151,8 @@ int intattn_cache_write(const intattn_rows_t* k, const intattn_rows_t* v, const 
   if (B < 0 || Hkv <= 0 || L < 0 || Lmax < 0 || !scales || (q != nullptr) != (q_out != nullptr) || (q && H <= 0))
     return INTATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return INTATTN_ERR_UNSUPPORTED;
-  if (dtype != INTATTN_DTYPE_FP16 && dtype != INTATTN_DTYPE_BF16) return INTATTN_ERR_UNSUPPORTED;
+  int32_t bf16, zero;
+  if (!row_dtype(dtype, &bf16, &zero)) return INTATTN_ERR_UNSUPPORTED;
   if (bits != 8 && bits != 4) return INTATTN_ERR_UNSUPPORTED;
   if (Hkv > 65535 || (q && H > 65535)) return INTATTN_ERR_UNSUPPORTED;
   if (scales->per_head && (Hkv > INTATTN_MAX_HEADS || (q && H > INTATTN_MAX_HEADS))) return INTATTN_ERR_UNSUPPORTED;
@@ -185,7 +196,8 @@ int intattn_cache_write(const intattn_rows_t* k, const intattn_rows_t* v, const 
   a.B = B;
   a.L = L;
   a.Lmax = Lmax;
-  a.bf16 = dtype == INTATTN_DTYPE_BF16 ? 1 : 0;
+  a.bf16 = bf16;
+  a.zero_left_out = zero;
   a.per_head = scales->per_head ? 1 : 0;
   a.start = start;
   a.lengths = lengths;
@@ -198,7 +210,8 @@ int intattn_cache_read(const void* k_cache, const void* v_cache, const intattn_s
   if (B < 0 || Hkv <= 0 || L < 0 || Lmax < 0 || !scales || (v_cache != nullptr) != (v_out != nullptr))
     return INTATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return INTATTN_ERR_UNSUPPORTED;
-  if (dtype != INTATTN_DTYPE_FP16 && dtype != INTATTN_DTYPE_BF16) return INTATTN_ERR_UNSUPPORTED;
+  int32_t bf16, zero;
+  if (!row_dtype(dtype, &bf16, &zero)) return INTATTN_ERR_UNSUPPORTED;
   if (bits != 8 && bits != 4) return INTATTN_ERR_UNSUPPORTED;
   if (scales->per_head && Hkv > INTATTN_MAX_HEADS) return INTATTN_ERR_UNSUPPORTED;
   ReadArgs a;
@@ -223,7 +236,8 @@ int intattn_cache_read(const void* k_cache, const void* v_cache, const intattn_s
   a.H = Hkv;
   a.L = L;
   a.Lmax = Lmax;
-  a.bf16 = dtype == INTATTN_DTYPE_BF16 ? 1 : 0;
+  a.bf16 = bf16;
+  a.zero_left_out = zero;
   a.per_head = scales->per_head ? 1 : 0;
   a.bits = bits;
   a.asym_k = scales->z_k ? 1 : 0;

@@ -118,6 +118,8 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
       Lp + Lmax < 1 || Lp + Lmax > 65535)
     return INTATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return INTATTN_ERR_UNSUPPORTED;
+  const bool zero_left_out = out_dtype >= 0 && (out_dtype & INTATTN_ZERO_LEFT_OUT);
+  if (zero_left_out) out_dtype &= ~INTATTN_ZERO_LEFT_OUT;
   if (out_dtype != INTATTN_DTYPE_INT8 && out_dtype != INTATTN_DTYPE_FP16 && out_dtype != INTATTN_DTYPE_BF16)
     return INTATTN_ERR_UNSUPPORTED;
   if (!scales) return INTATTN_ERR_INVALID_ARG;
@@ -160,6 +162,7 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   a.row_tiles = (a.R + intattn::shared::kBM - 1) / intattn::shared::kBM;
   a.per_head = scales->per_head ? 1 : 0;
   a.out_kind = out_dtype;
+  a.zero_left_out = zero_left_out ? 1 : 0;
   a.k_u8 = scales->z_k ? 1 : 0;
   a.v_u8 = scales->z_v ? 1 : 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -94,6 +94,7 @@ struct SharedArgs {
   int32_t seg_cost;              // of a segment, in tiles, for equal shares (see first_tile)
   int32_t cta_cost, cta_more;    // a CTA's share of the cost, and one more for the first cta_more
   int32_t none;                  // 0 (see OwnRing)
+  int32_t zero_left_out;         // outputs of a sequence whose length is out of range become 0
   float s_o[INTATTN_MAX_HEADS];
   uint32_t lut[INTATTN_MAX_CLIPS][32];
   HeadParamsDev hp[INTATTN_MAX_HEADS];
@@ -639,9 +640,11 @@ __device__ __forceinline__ void finish(const SharedArgs& a, const HeadParamsDev*
   for (long long i = thread; i < n; i += threads) {
     const int row = static_cast<int>(i / (D / 4)), c = 4 * static_cast<int>(i % (D / 4));
     const int hk = row / a.R, r = row - hk * a.R, b = r / a.G, h = hk * a.G + (r - b * a.G);
+    bool skip = false;
     if (a.lengths != nullptr) {
       const int len = __ldg(a.lengths + b);
-      if (len < 0 || len > a.Lmax) continue;
+      skip = len < 0 || len > a.Lmax;
+      if (skip && !a.zero_left_out) continue;
     }
     const float4 v = __ldcg(reinterpret_cast<const float4*>(a.acc + static_cast<size_t>(row) * D + c));
     const HeadParamsDev hp = hp_s[a.per_head ? h : 0];
@@ -650,7 +653,7 @@ __device__ __forceinline__ void finish(const SharedArgs& a, const HeadParamsDev*
     int32_t y[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      y[k] = static_cast<int8_t>(prefill::requant_byte(static_cast<int32_t>(f[k]) - fix, hp.Mo, hp.so));
+      y[k] = skip ? 0 : static_cast<int8_t>(prefill::requant_byte(static_cast<int32_t>(f[k]) - fix, hp.Mo, hp.so));
     const size_t at = (static_cast<size_t>(b) * a.H + h) * D + c;
     if (a.out_kind == INTATTN_DTYPE_INT8) {
       *reinterpret_cast<uint32_t*>(static_cast<int8_t*>(a.out) + at) = prefill::pack4(
