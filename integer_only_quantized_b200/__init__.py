@@ -7,6 +7,7 @@ fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -522,25 +523,25 @@ class _On:
     allocates belongs to the stream it runs on; gives the stream's handle."""
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, []
+        self.device, self.stream = device, stream
 
     def __enter__(self) -> int:
         import torch
-        if getattr(self.stream, "device", self.device) != self.device:
-            raise ValueError(f"stream is on {self.stream.device}, the tensors are on {self.device}")
-        self.guards.append(torch.cuda.device(self.device))
-        self.guards[0].__enter__()
         s = self.stream
-        if s is not None:
-            if not hasattr(s, "cuda_stream"):
-                s = torch.cuda.ExternalStream(int(s), device=self.device)
-            self.guards.append(torch.cuda.stream(s))
-            self.guards[1].__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        if getattr(s, "device", self.device) != self.device:
+            raise ValueError(f"stream is on {s.device}, the tensors are on {self.device}")
+        if s is not None and not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(getattr(s, "cuda_stream", s)), device=self.device)
+        with contextlib.ExitStack() as guards:  # left again where a step on the way in fails
+            guards.enter_context(torch.cuda.device(self.device))
+            if s is not None:
+                guards.enter_context(torch.cuda.stream(s))
+            handle = torch.cuda.current_stream(self.device).cuda_stream
+            self.guards = guards.pop_all()
+        return handle
 
     def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+        self.guards.__exit__(*exc)
 
 
 class _Here:
