@@ -337,10 +337,14 @@ struct Unit {
 };
 
 // A warp's private ring of blocks for the own rows' tiles.  The warp that reads a
-// block also starts the copy that replaces it, and nothing but a dependency orders a
-// copy behind reads that are still on their way to registers (the two take
-// different paths; with other warps keeping shared memory busy a copy did overtake them).  So
-// `issue` takes a value made of what was read: `read` & args.none, which is 0 when it arrives.
+// block also starts the copy that replaces it, so the copy (async proxy) has to come after every
+// lane's reads (generic proxy): each lane's proxy fence, then the warp's barrier, then
+// one lane's copy.  That lane's own reads moreover reach it as a value: `issue` takes
+// one made of what was read, `read` & args.none, which is 0 when it arrives.  Without
+// any of this a copy did overtake reads still on their way to registers, with
+// other warps keeping shared memory busy.  Fence and barrier cost little beside that value:
+// LLaMA-7B heads, B64, up to 777 own keys 68.1 us a call (68.0 without them), B64 H32/8 over
+// 8192 + 1024 keys 42.5 (41.7), up to 8192 own keys of H32/8 alone 142.5 (142.7).
 struct OwnRing {
   uint32_t base, bar;    // shared addresses: slot i at base + kOwnBytes i, barrier i at bar + 8 i
   uint32_t slots;
@@ -349,6 +353,8 @@ struct OwnRing {
   __device__ __forceinline__ uint32_t slot(uint32_t n) const { return n < slots ? n : n - slots; }
   __device__ __forceinline__ void issue(const CUtensorMap* tm, int y, int z, uint32_t zero) {
     const uint32_t i = slot(issued);
+    fence_proxy_async_smem();
+    __syncwarp();
     tma_load_3d_elect(base + kOwnBytes * i + zero, tm, bar + 8 * i + zero, kOwnBytes, 0, y, z);
     issued = step(issued);
   }
