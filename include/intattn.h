@@ -433,7 +433,8 @@ typedef struct intattn_rope_norm {
  * INTATTN_DTYPE_FP16 or INTATTN_DTYPE_BF16) into q_out and k_out of the same type, one
  * rounding per element: what intattn_quantize and intattn_forward_fp take.
  * Hkv == 0 with k == k_out == NULL: queries only.  In place (an output equal
- * to its input, strides too) is allowed, any other overlap is not.  One
+ * to its input, strides too) is allowed, any other overlap is not: an output that
+ * starts at the address of another tensor is refused (INTATTN_ERR_INVALID_ARG).  One
  * launch, asynchronous on `stream`. */
 int intattn_qk_norm_rope(const intattn_rows_t *q, const intattn_rows_t *k, const intattn_rope_norm_t *rn, int dtype,
                          int B, int H, int Hkv, int L, int d, const intattn_rows_t *q_out,
@@ -456,6 +457,7 @@ int intattn_qk_norm_rope(const intattn_rows_t *q, const intattn_rows_t *k, const
  *   q_out [B, H, L, d] int8.  Every other row is left as it was.  A cache row outside
  *   [0, Lmax) is not written (nor its q_out row) and is reported by
  *   intattn_device_error (INTATTN_ERR_PARAM_RANGE).
+ *   k_cache, v_cache and q_out do not overlap (INTATTN_ERR_INVALID_ARG).
  * One launch, asynchronous on `stream`. */
 int intattn_cache_write(const intattn_rows_t *k, const intattn_rows_t *v, const intattn_rows_t *q, int dtype,
                         const intattn_scales_t *scales, int bits, const intattn_rope_norm_t *rn, int B, int H,
@@ -465,7 +467,8 @@ int intattn_cache_write(const intattn_rows_t *k, const intattn_rows_t *v, const 
 /* The values of cache rows: row t < lengths[b] (NULL: L) of sequence b of
  * k_out, v_out [B, Hkv, L, d] (contiguous, dtype fp16 or bf16) receives
  * RN(RN32(s (code - z))) of cache row start[b] + t.  scales, bits, start, lengths and rows out
- * of range: as intattn_cache_write.  v_cache == v_out == NULL: K only.  One
+ * of range: as intattn_cache_write.  v_cache == v_out == NULL: K only.  k_out and
+ * v_out do not overlap (INTATTN_ERR_INVALID_ARG).  One
  * launch, asynchronous on `stream`. */
 int intattn_cache_read(const void *k_cache, const void *v_cache, const intattn_scales_t *scales, int bits, int B,
                        int Hkv, int L, int Lmax, int d, const int32_t *start, const int32_t *lengths, int dtype,

@@ -29,6 +29,18 @@ int check_rows(const intattn_rows_t* r, int B, int heads, int L, bool output) {
   return INTATTN_OK;
 }
 
+// Whether n bytes at a and m bytes at b share any.
+bool overlap(const void* a, unsigned long long n, const void* b, unsigned long long m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < n : x - y < m;
+}
+
+// Whether the rows of x are those of y, one by one.
+bool same_rows(const intattn_rows_t* x, const intattn_rows_t* y, int B, int heads, int L) {
+  return x->ptr == y->ptr && (B <= 1 || x->stride_b == y->stride_b) && (heads <= 1 || x->stride_h == y->stride_h) &&
+         (L <= 1 || x->stride_l == y->stride_l);
+}
+
 int check_rope_norm(const intattn_rope_norm_t* rn, int d, RowArgs* a) {
   if (rn->positions && !rn->table) return INTATTN_ERR_INVALID_ARG;
   if (rn->table) {
@@ -137,6 +149,14 @@ int intattn_qk_norm_rope(const intattn_rows_t* q, const intattn_rows_t* k, const
     a.t[i].w = i ? rn->w_k : rn->w_q;
     a.t[i].rope = 1;
   }
+  // An output that starts where another tensor does: only in place.  (Views of
+  // one packed buffer interleave, so their extents say nothing.)
+  for (int i = 0; i < a.n_tensors; ++i)
+    for (int j = 0; j < a.n_tensors; ++j) {
+      if (i == j ? out[i]->ptr == in[i]->ptr && !same_rows(out[i], in[i], B, heads[i], L)
+                 : out[i]->ptr == in[j]->ptr || out[i]->ptr == out[j]->ptr)
+        return INTATTN_ERR_INVALID_ARG;
+    }
   a.B = B;
   a.L = L;
   a.bf16 = bf16;
@@ -193,6 +213,11 @@ int intattn_cache_write(const intattn_rows_t* k, const intattn_rows_t* v, const 
     t.lo = asym ? 0.0f : -t.hi;
     t.sc = i * S;
   }
+  const unsigned long long cache = static_cast<unsigned long long>(B) * Hkv * Lmax * (d * bits / 8);
+  const unsigned long long queries = static_cast<unsigned long long>(B) * H * L * d;
+  if (overlap(k_cache, cache, v_cache, cache) ||
+      (q && (overlap(q_out, queries, k_cache, cache) || overlap(q_out, queries, v_cache, cache))))
+    return INTATTN_ERR_INVALID_ARG;
   a.B = B;
   a.L = L;
   a.Lmax = Lmax;
@@ -227,6 +252,8 @@ int intattn_cache_read(const void* k_cache, const void* v_cache, const intattn_s
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(start) ||
       !aligned4(lengths))
     return INTATTN_ERR_UNSUPPORTED;
+  const unsigned long long values = 2ull * B * Hkv * L * d;
+  if (v_out && overlap(k_out, values, v_out, values)) return INTATTN_ERR_INVALID_ARG;
   a.in[0] = static_cast<const uint8_t*>(k_cache);
   a.in[1] = static_cast<const uint8_t*>(v_cache);
   a.out[0] = k_out;
