@@ -450,7 +450,8 @@ int intattn_qk_norm_rope(const intattn_rows_t *q, const intattn_rows_t *k, const
  *   becomes the code of 0.
  *   scales: s_k, s_v (and z_k, z_v) hold Hkv entries per head, s_q H; s_o and clip_c are not
  *   read.  rn != NULL: norm and rotation of q and k (not v) come
- *   first, in fp32 without a rounding between.
+ *   first, in fp32 without a rounding between; a token whose position is negative or past the
+ *   table is left out whole, its V row too.
  *   Row t of sequence b, t < lengths[b] (DEVICE int32 [B]; NULL: L), goes to
  *   cache row start[b] + t (DEVICE int32 [B]) of k_cache, v_cache [B, Hkv, Lmax, d]
  *   (bits = 4: d/2 bytes a row, packed as intattn_decode_int4 reads them), and to row t of

@@ -721,7 +721,8 @@ def cache_write(k, v, scales: Scales, k_cache, v_cache, start, lengths=None, bit
     zero-points), or, bits = 4, uint8 [B, Hkv, Lmax, d/2].  q [B, H, L, d]:
     also the step's queries, with scales.s_q, into int8 q_out (returned; new
     where none is passed, with 0 in the rows that are not written).
-    norm: norm and rotation of q and k first, in the same pass."""
+    norm: norm and rotation of q and k first, in the same pass; a token whose
+    position is negative or past the table is left out whole, its V row too."""
     import torch
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise TypeError("k must be a CUDA tensor [B, Hkv, L, d]")
