@@ -65,7 +65,7 @@ struct RowArgs {
   int32_t zero_left_out;       // rows left out (padding, out of range) of outputs other than a cache become 0
   float eps;
 };
-// with codes: 6 KB more, which a call without them need not hand over
+// with codes: 3 KB more, which a call without them need not hand over
 struct RowCodeArgs : RowArgs {
   float inv[3 * INTATTN_MAX_HEADS];    // RN32(1 / scale)
   float zero[3 * INTATTN_MAX_HEADS];   // zero-points (0: symmetric)

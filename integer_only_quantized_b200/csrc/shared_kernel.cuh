@@ -114,7 +114,7 @@ constexpr int kTeams = 2;                  // softmax teams taking alternate til
 constexpr int kSoftWarps = 16;
 constexpr int kTeamWarps = kSoftWarps / kTeams;
 constexpr int kCols = 64;                  // S columns per thread and tile (two halves)
-constexpr int kChunk = 16;                 // of them read from TMEM at a time
+constexpr int kChunk = 16;                 // of them read from TMEM at a time (tmem_ld16, tmem_st4)
 constexpr int kProducerWarp = 16;
 constexpr int kMmaWarp = 17;               // issues S = Q.K^T
 constexpr int kPvWarp = 18;                // issues O += P.V
@@ -205,11 +205,6 @@ __device__ __forceinline__ int folds_at(const SharedArgs& a, int j) { return min
 
 __device__ __forceinline__ uint32_t bias(int32_t s) { return static_cast<uint32_t>(s) ^ 0x80000000u; }
 __device__ __forceinline__ int32_t unbias(uint32_t u) { return static_cast<int32_t>(u ^ 0x80000000u); }
-
-__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld32(taddr, v); }
-__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld16(taddr, v); }
-__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&v)[8]) { tmem_st8(taddr, v); }
-__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&v)[4]) { tmem_st4(taddr, v[0], v[1], v[2], v[3]); }
 
 // Four fp32 adds to consecutive addresses (16-byte aligned).
 __device__ __forceinline__ void red_add4(float* p, float a, float b, float c, float d) {
@@ -859,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
 #pragma unroll 1
       for (int c = 0; c < kCols / kChunk; ++c) {
         uint32_t v[kChunk];
-        ld_cols(trow + kColS + buf * kBN + kChunk * c, v);
+        tmem_ld16(trow + kColS + buf * kBN + kChunk * c, v);
         tmem_wait_ld();
         if (c == kCols / kChunk - 1) {
           tc_fence_before();
@@ -1003,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
                 const uint32_t phase = psets == 1 ? ((pi + 1) >> 1) - 1 : (pi >> set_bits) - 1;  // pi = 0 .. psets - 1: none yet
                 if (!mbar_wait_warp(bar(kBarPEmpty + e), phase & 1, kRoleSoftmax)) ok = false;
               }
-              st_cols(tlane + kColP + pb * 32 + half * (kCols / 4) + c * (kChunk / 4), pw);
+              tmem_st4(tlane + kColP + pb * 32 + half * (kCols / 4) + c * (kChunk / 4), pw[0], pw[1], pw[2], pw[3]);
             });
             if (!got) ok = false;
             if (!ok) break;
