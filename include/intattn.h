@@ -444,7 +444,8 @@ int intattn_qk_norm_rope(const intattn_rows_t *q, const intattn_rows_t *k, const
  * written (the scales intattn_decode and intattn_decode_int4 read the cache
  * with), and optionally the step's queries.
  *   k, v [B, Hkv, L, d], q [B, H, L, d] or NULL: dtype fp16 or bf16.
- *   code = clamp(rint(RN32(x RN32(1 / s))) + z, lo, hi), ties to even;
+ *   code = clamp(rint(RN32(x RN32(1 / s))) + z, lo, hi), ties to even (a
+ *   reciprocal past fp32's range is its largest number);
  *   symmetric (no zero-points): z = 0, [lo, hi] = [-127, 127] or, bits = 4,
  *   [-7, 7]; with zero-points: [0, 255] or [0, 15].  An infinity saturates, a NaN
  *   becomes the code of 0.
@@ -489,15 +490,18 @@ size_t intattn_decode_shared_workspace_size(int B, int H, int Hkv, int Lmax, int
  *   q [B, H, 1, d] int8; k_prefix, v_prefix [Hkv, Lp_max, d], the first Lp rows valid;
  *   k_cache, v_cache [B, Hkv, Lmax, d]; int8, or u8 with zero-points (prefix and
  *   caches share scales and zero-points).
- *   lengths: DEVICE int32 [B], 0 <= lengths[b] <= Lmax, or NULL: Lmax.  A length out of
+ *   lengths: DEVICE int32 [B], 0 <= lengths[b] <= Lmax, or NULL: Lmax; read more than once,
+ *   so nothing may change them before the call has finished.  A length out of
  *   range leaves the sequence's output unwritten and is reported by
  *   intattn_device_error (INTATTN_ERR_PARAM_RANGE).  A sequence without any
  *   key gives 0.
- *   1 <= Lp + Lmax <= 65535; with Lp (Lmax) 0 the prefix (cache) may be NULL.
+ *   1 <= Lp + Lmax <= 65535 (whatever the lengths: the host does not see them); with Lp (Lmax) 0 the
+ *   prefix (cache) may be NULL.
  *   out [B, H, 1, d]: out_dtype INTATTN_DTYPE_INT8: the codes of the definition; INTATTN_DTYPE_FP16
  *   or INTATTN_DTYPE_BF16: the values RN(RN32(s_o code)) they stand for.
  *   workspace: device, 256-byte aligned, at least
- *   intattn_decode_shared_workspace_size bytes; contents need no
+ *   intattn_decode_shared_workspace_size bytes (about 5 B H Lmax + 4 B H d: a score
+ *   and an index byte for each query head and row of capacity); contents need no
  *   initialisation; calls (and graphs) that share it must be ordered on one
  *   stream.  Return codes: as intattn_decode. */
 int intattn_decode_shared(const int8_t *q, const int8_t *k_prefix, const int8_t *v_prefix, int Lp, int Lp_max,

@@ -71,9 +71,9 @@ void set_input(RowTensor* t, const intattn_rows_t* r, int heads) {
 // A warp takes a batch of one tensor's heads of a token: as many as it holds in
 // flight (D / 8 lanes and four loads per lane) when that still gives every SM
 // several warps, else one load's worth, so that few tokens spread over more SMs.
-// Always four loads: one token 2.8 us instead of 2.5, the cache step of 64 sequences with
-// eight K / V heads 6.4 instead of 5.4; always one: the rows of a LLaMA-7B
-// prefill 104 us instead of 52.
+// Always four loads: one token 2.9 us instead of 2.4, the cache write of 64 tokens with
+// eight K / V heads 3.7 instead of 2.8; always one: the rows of a LLaMA-7B
+// prefill 101 us instead of 51, their cache write 177 instead of 91.
 template <bool kCodes>
 int rows_launch(intattn::RowCall<kCodes>& a, int d, cudaStream_t st) {
   int sms = 0;

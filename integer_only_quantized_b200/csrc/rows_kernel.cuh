@@ -13,14 +13,19 @@
 //             f + rot/2, or neighbours where pairs are interleaved), so the rotation
 //             needs no other lane: with eight consecutive channels per lane
 //             and a shuffle per channel the rows of a LLaMA-7B prefill (B1
-//             H32/32 L8192 d128 bf16) took 82 us instead of 64
+//             H32/32 L8192 d128 bf16) took 82 us instead of
+//             64, both before the paired arithmetic
 //   codes     clamp(rint(RN32(y inv)) + z), or one rounding to fp16 / bf16
 // All of it is bound by memory (2 bytes in, 2, 1 or 1/2 byte out per channel),
 // closely followed by the instructions in between; for the few rows of a
 // decode step by the launch and one round trip.  Measured, per call in a CUDA graph:
-// those LLaMA-7B rows, norm and rotation, 52.3 us (5.2 TB/s; a copy of the bytes
-// takes 41.7); one token of 12 heads 2.5 us; the write of B4 L4096 H32 d128
-// rows as int8 92 us and their read-back 60 us (5.3 TB/s together; floor 123).  In fp32
+// those LLaMA-7B rows, norm and rotation, 51.3 us (5.3 TB/s; a copy of the bytes
+// takes 41.7); one token of 12 heads 1.8 us.  B4 L4096 H32 d128 K and V rows, beside the
+// copy of each direction's own bytes:
+//   write  int8 93.4 us (61.5), u8 91.2, with the keys' norm and rotation 108.5, and
+//          with the queries too 167.8 (92.3); int4 99.1 (51.3), with zero-points the same
+//   read   int8 or u8 62.0 us (61.5), int4 56.5 (51.3)
+// The write is bound by its instructions (76 % of the issue slots), the read by memory.  In fp32
 // pairs (mul2, fma2) norm and rotation went from 64 to 57 us, with four loads
 // per lane and a tensor per grid row to 52.7; two, six or eight loads per
 // lane, and 64 or 256 threads, were slower.
@@ -169,7 +174,7 @@ __device__ __forceinline__ void codes4(const float2 (&y)[2], float inv, float lo
 
 // 0 into the warp's output rows, which the call leaves out (not those of a
 // cache).  A function of its own, finding everything again: inlined beside the kernel's
-// loop it made the write of a LLaMA-7B prompt 99.6 us instead of 93.3.
+// loop it made the write of a LLaMA-7B prompt 99.6 us instead of 93.3, which leaves nothing out.
 template <int D, bool kCodes>
 __device__ __noinline__ void zero_rows(const RowCall<kCodes>& a) {
   constexpr int kLpr = D / 8;

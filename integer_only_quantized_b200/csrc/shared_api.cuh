@@ -169,8 +169,10 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   int sms = 0;
   if (sm_count(&sms) != INTATTN_OK) return INTATTN_ERR_CUDA;
   // Few queries fold F key tiles into a tile, as long as every SM still gets
-  // one: B9 H32/8 d128 over 50000 shared keys 51 us a call, without folding 63 us;
-  // B4 H12 d64 over 500 (too few tiles) 17.2 us, folded all the same 17.5 us.
+  // one: B9 H32/8 d128 over 50000 shared keys 48.0 us a call, without folding 61.3;
+  // B2 H32/8 over 30000 35.1, without 43.7; B8 H12 d64 over 9000 25.3, without 31.3.  Too
+  // few tiles: B4 H12 d64 over 500 18.0 us, folded all the same 18.5; B16 H32/8 over 2000
+  // 29.1 and 30.6; one shape the other way, B16 H16 d64 over 1500 20.7 and 19.8.
   a.fold = 1;
   for (int f = 2; f <= 4; f *= 2)
     if (a.R <= intattn::shared::kBM / f && static_cast<long long>(Hkv) * ((a.key_tiles + f - 1) / f) >= sms) a.fold = f;
@@ -187,8 +189,11 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
     return INTATTN_ERR_CUDA;
   // The K / V ring and the own warps' rings share their memory (kRingBytes):
   // one block per own warp instead of two where the prefix is the longer stream
-  // (B9 H32/8 over 50000 shared and up to 333 own keys: 51.0 us against 52.5 with
-  // two; one everywhere: B64 H32, 4001 shared and up to 777 own keys 82 us against 67.5).
+  // (B9 H32/8 over 50000 shared and up to 333 own keys: 48.0 us against 48.9 with
+  // two; one everywhere: B64 H32, 4001 shared and up to 777 own keys 84.0 us against 68.4, B64
+  // H32/8 over up to 8192 own keys 173 against 142).  The rule knows the caches' capacity, not
+  // the lengths on the device; caches of 8192 rows that hold 100 (B64 H32/8, 8192 shared): two
+  // blocks 35.9 us, one 36.5.
   const long long own_keys = static_cast<long long>(B) * Hkv * Lmax, prefix_keys = static_cast<long long>(Hkv) * Lp;
   a.own_slots = Lmax == 0 ? 0 : 2 * own_keys <= prefix_keys ? 1 : 2;
   a.stages = (intattn::shared::kRingBytes - a.own_slots * intattn::shared::kOwnWarps * intattn::shared::kOwnBytes) /
@@ -197,9 +202,10 @@ int intattn_decode_shared(const int8_t* q, const int8_t* k_prefix, const int8_t*
   const long long own = static_cast<long long>(B) * Hkv * ((Lmax + 127) / 128);
   const int grid = static_cast<int>(std::min<long long>(sms, std::max<long long>(std::max(tiles, own), 1)));
   // A CTA whose tiles belong to two heads pays for the second segment (tables, O read out
-  // twice): four tiles' worth.  B64 H32/8 over 8192 + 1024 keys 44.4 us a call instead
-  // of 47.5, B9 L50000 51.0 instead of 53.9.  Not where a CTA has one tile at
-  // most: B4 H12 L500 17.2 us, with it 18.9 (two tiles here, none there).
+  // twice): four tiles' worth.  B64 H32/8 over 8192 + 1024 keys 42.5 us a call instead
+  // of 46.0 without it (two tiles' worth 43.8, eight 42.8), B9 L50000 48.0 instead of 51.0, B128 H8 d64 over
+  // 16000 35.1 instead of 38.1, B30 H32 over 2400 29.2 instead of 32.4 (two 28.6, eight 33.1).  Not where a CTA has
+  // one tile at most: B4 H12 L500 18.0 us, with it 19.4 (two tiles here, none there).
   a.seg_cost = tiles > grid ? 4 : 0;
   const long long cost = static_cast<long long>(Hkv) * a.row_tiles * (a.seg_tiles + a.seg_cost);
   if (cost > 0x7fffffffll) return INTATTN_ERR_UNSUPPORTED;

@@ -42,16 +42,23 @@
 // (4 bytes per key and head), and from phase B on their table indices (one
 // byte), wait in the workspace; a warp reads back what it wrote itself.
 //
-// Measured, per call in a CUDA graph (zero kernel and this one; own lengths
-// uniform up to the number given), beside the time of a copy of the bytes:
-//   B4 H12/12 d64, 500 shared, 64 own            17.7 us   (launches and three
+// Measured, per call in a CUDA graph over several sets of inputs (zero kernel and this
+// one; own lengths uniform up to the number given), beside the time of a copy of the bytes:
+//   B4 H12/12 d64, 500 shared, 64 own            17.8 us   (launches and three
 //                                                phases of one tile each)
-//   B64 H32/8 d128, 8192 shared, 1024 own        45 us     12.9 us
-//   B64 H32/32 d128 u8, 4001 shared, 777 own     68 us     36.3 us (3.5 TB/s)
-//   B9 H32/8 d128, 50000 shared, 333 own         50 us     16.1 us
+//   B64 H32/8 d128, 8192 shared, 1024 own        45.6 us   12.9 us
+//   B64 H32/32 d128 u8, 4001 shared, 777 own     69.0 us   36.3 us (3.4 TB/s)
+//   B9 H32/8 d128, 50000 shared, 333 own         50.2 us   16.1 us
+//   B64 H32/8 d128, none shared, 8192 own        156.6 us  82.2 us
+//   B64 H64/8 d64, 500 shared, 8192 own          140.1 us  41.2 us
+//   B64 H32/32 d128, 500 shared, 8192 own        416 us    329 us
+// (The comparisons beside the rules below and in shared_api.cuh repeat a call on
+// the same inputs, so the smaller cases come partly from L2: 42.5, 68.4 and 48.0 us for
+// the second, third and fourth.)
 // Bound: the three dependent phases (scores of the prefix are made three
 // times), in each the latency of the softmax warps' loops and of fetching them: the issue
-// slots are a third used, the tensor pipe 9 to 21 %, DRAM 21 to 42 %.  Every
+// slots are a third used, the tensor pipe 9 to 21 %, DRAM 21 to 44 %.  Long own caches: the scores and index
+// bytes of every query head, 10 G bytes per key beside 2 d of K and V.  Every
 // change that made a loop's code smaller made it faster, and unrolling,
 // reading ahead and prefetching V into L2 during phase B made it slower.
 #pragma once
@@ -243,8 +250,9 @@ __device__ __forceinline__ int own_rows(const SharedArgs& a, int b) {
 // of eight query heads), in the order (b, unit, block), and a warp's
 // place among them.  Warp-collective.
 // Blocks' worth of work in changing the unit, for equal shares.  LLaMA-7B heads, B64,
-// up to 777 own keys: 67.4 us a call; with 1 70.0 us.  B64 H32/8, up to 1024 own
-// keys: 44.5 us; with 3 44.9 us.
+// up to 777 own keys: 68.4 us a call, with 1 71.7, with 3 67.9; B64 H64/8 d64, up to 8192:
+// 142.2, with 1 141.4, with 3 144.0; B32 H12 d64, up to 500: 21.5, 20.9, 21.8.  Twelve other shapes differ by 2 %
+// or less.
 constexpr int kUnitCost = 2;
 struct Walk {
   int b, hk, g, blk, nb;  // sequence, K / V head, group of eight query heads; nb: blocks of the sequence
@@ -393,8 +401,8 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int c) {
 // A = K: sixteen keys by 32 channels per product; B: the unit's queries.  A key
 // past the sequence's last (in a started 16-key step) gets the lowest score, whose table
 // entry is 0.  The loop is as short as it can be: with the next step's fragments read
-// ahead (more code) LLaMA-7B heads, B64, 4001 shared and up to 777 own keys took 69.5 us
-// a call instead of 67.5.
+// ahead (more code) LLaMA-7B heads, B64, 4001 shared and up to 777 own keys took 3 %
+// longer.
 template <int D>
 __device__ __forceinline__ bool own_scores(const SharedArgs& a, bool k_u8, OwnRing& ring, Walk w, int n) {
   constexpr int kKeys = kOwnBytes / D;
@@ -488,7 +496,7 @@ struct RowIndex {
 // take the unit's rows, and with fewer than eight rows several steps.  The next
 // step's scores are on their way while this one's are worked on.  One step per turn of
 // the loop: with four unrolled (more loads in flight, more code to fetch)
-// LLaMA-7B heads, B64, 4001 shared and up to 777 own keys took 72.2 us a call instead of 70.3.
+// LLaMA-7B heads, B64, 4001 shared and up to 777 own keys took 3 % longer.
 template <int D>
 __device__ __forceinline__ void own_sums(const SharedArgs& a, const HeadParamsDev* hp_s, const uint32_t* lut_s, Walk w,
                                          int n) {
@@ -547,8 +555,7 @@ __device__ __forceinline__ int own_pv_start(const SharedArgs& a, OwnRing& ring, 
 // ---- phase C of the own rows: P.V of the same blocks ----
 // A = V^T: sixteen channels by 32 keys per product, transposed on the way from
 // shared memory; B = P: query row n8, keys 4 t .. + 3 and 16 + 4 t .. + 3, made
-// while V is read (made a step ahead, with more code: 71.2 us a call instead of 69.7
-// in the case above).
+// while V is read (made a step ahead, with more code: 2 % longer in the case above).
 template <int D>
 __device__ __forceinline__ bool own_pv(const SharedArgs& a, bool v_u8, OwnRing& ring, const HeadParamsDev* hp_s,
                                        const uint32_t* lut_s, Walk w, Walk ld, int left, int n) {
@@ -1132,8 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_kernel(const __grid_consta
     // dependent instructions, in which the tensor pipe stands still: so one
     // thread runs the whole loop, and waits for a K or V tile only before its
     // own products, while those of the one before it run (warp-wide loops: B9
-    // L50000 54.7 us a call instead of 53.8).  Two issuers instead of one took B64 L8192 from
-    // 52 to 50.6 us and left the other cases where they were.
+    // L50000 2 % longer).  Two issuers instead of one took 3 % from B64 L8192 and left the other cases where they were.
     if (elect_one()) {
       const bool pv = warp == kPvWarp;
       const uint64_t kv_desc0 = smem_desc(sKV, 16, C::kSBO, C::kSwizzle);
