@@ -19,7 +19,7 @@
 // All of it is bound by memory (2 bytes in, 2, 1 or 1/2 byte out per channel),
 // closely followed by the instructions in between; for the few rows of a
 // decode step by the launch and one round trip.  Measured, per call in a CUDA graph:
-// those LLaMA-7B rows, norm and rotation, 51.3 us (5.3 TB/s; a copy of the bytes
+// those LLaMA-7B rows, norm and rotation, 51.2 us (5.3 TB/s; a copy of the bytes
 // takes 41.7); one token of 12 heads 1.8 us.  B4 L4096 H32 d128 K and V rows, beside the
 // copy of each direction's own bytes:
 //   write  int8 93.4 us (61.5), u8 91.2, with the keys' norm and rotation 108.5, and
